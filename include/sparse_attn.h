@@ -26,6 +26,13 @@
  *   sa_shard_lengths, sa_shard_selection, sa_merge_states
  *                     sequence sharding: page ranges per shard, merged states
  *
+ * Around the sparse step, for a model's layers:
+ *   sa_append_kv_rope RMS norm and rotation of queries and keys, then the append
+ *   sa_paged_decode   one new token over the whole cache, or a sliding window of
+ *                     it and its first tokens
+ *   sa_paged_prefill  a prompt's (or a chunk's) tokens over the cache, causal,
+ *                     with the same window
+ *
  * Sources (cited by page title and section):
  *   [vortex]  "flow: add H2O sparse attention (page-level and token-level,
  *             MHA + GQA)", vortex_torch pull request 6.
@@ -91,6 +98,7 @@ typedef enum sa_dtype { SA_BF16 = 0, SA_FP16 = 1 } sa_dtype;
 #define SA_DEV_OVERFLOW 2   /* table or retained-list capacity exceeded; the excess was dropped */
 #define SA_DEV_BAD_COUNT 4  /* a selection / retained count outside [0, stride] (clamped) */
 #define SA_DEV_TIMEOUT 8    /* a bounded wait inside a kernel gave up (the kernel stopped early) */
+#define SA_DEV_BAD_POSITION 16  /* a rotary position outside [0, max_pos) (the row's pair is not turned) */
 
 /* The paged cache: pools plus per-page statistics. */
 typedef struct sa_cache {
@@ -590,6 +598,113 @@ sa_status sa_shard_selection(const int32_t* sel_idx, const int32_t* sel_cnt, int
 sa_status sa_merge_states(const void* o_parts, const float* lse_parts, int32_t num_shards, int32_t rows,
                           int32_t head_dim, int32_t dtype, void* out, float* lse, void* stream);
 
+/* Norm and rotation of queries and keys, for sa_append_kv_rope. */
+typedef struct sa_rope {
+  const float* table;       /* [max_pos, rot_dim]: row p holds cos(p f_i) for the rot_dim / 2 pairs i,
+                               then sin(p f_i); may be NULL when rot_dim is 0 */
+  const int32_t* positions; /* nullable [num_axes, num_tokens]: each token's position on each axis;
+                               NULL (one axis): its place in the sequence */
+  const void* q_weight;     /* nullable [head_dim], dtype: RMS norm of each query head before the turn */
+  const void* k_weight;     /* nullable [head_dim], dtype: the same for keys */
+  int32_t max_pos;
+  int32_t rot_dim;          /* columns of a head that are turned, the first ones: 0, 4, 8, .. head_dim */
+  int32_t interleaved;      /* 0: pair i is columns (i, i + rot_dim / 2); otherwise (2i, 2i + 1) */
+  int32_t num_axes;         /* 1 .. 4 */
+  int32_t sections[4];      /* num_axes > 1: consecutive pairs that turn by each axis, rot_dim / 2 in all */
+  float eps;                /* of the norms */
+} sa_rope;
+
+/*
+ * sa_append_kv_rope -- norm and rotation of the queries and keys of new tokens,
+ * then sa_append_kv of the turned keys and the values, in one pass over them.
+ *
+ * Each head's row x of q and k_new becomes x * w / sqrt(mean(x^2) + eps) where
+ * its weights are given, then each pair (u, v) of its first rot_dim columns
+ * becomes (u cos - v sin, u sin + v cos) at the token's position on the pair's
+ * axis; float32, rounded once to dtype. Turned queries go to q_out, turned keys
+ * and the values to the pools, and the statistics (cache->meta, and cache->kstd
+ * where kept), hh, ret_pos and ret_cnt are those of sa_append_kv of them.
+ *   q, k_new, v_new  [num_tokens, heads, head_dim], dtype; consecutive tokens
+ *             q_stride, k_stride, v_stride elements apart (multiples of 8, at
+ *             least a token's heads), heads contiguous: slices of one
+ *             projection's output need no copy
+ *   q         nullable (with q_out): keys and values alone
+ *   num_q_heads  any count (not only a multiple of num_kv_heads)
+ *   new_cu, max_new_per_req  as sa_append_kv; new_cu[batch] <= num_tokens, and
+ *             rows from there on are padding: neither read nor written
+ *   advanced  0: the new tokens follow the seq_lens[b] cached ones, and
+ *             seq_lens[b] += n_b at the end; otherwise seq_lens already counts
+ *             them (as for sa_h2o_prefill) and is left alone, so that the layers
+ *             of a model can share one batch
+ *   q_out     [num_tokens, num_q_heads, head_dim], dtype, contiguous; may be q
+ *             itself where q is contiguous
+ * All data pointers, rope->table and the weights start on 16-byte boundaries. A
+ * request whose new_cu is not increasing within [0, num_tokens] or whose length
+ * is below its new tokens sets SA_DEV_BAD_COUNT and is skipped; tokens beyond
+ * the table row or max_new_per_req set SA_DEV_OVERFLOW and are dropped, queries
+ * too; a page with a bad block id sets SA_DEV_BAD_BLOCK and drops its keys and
+ * values.
+ */
+sa_status sa_append_kv_rope(const sa_cache* cache, const sa_batch* batch, const sa_rope* rope, const void* q,
+                            int64_t q_stride, int32_t num_q_heads, const void* k_new, int64_t k_stride,
+                            const void* v_new, int64_t v_stride, const int32_t* new_cu, int32_t num_tokens,
+                            int32_t max_new_per_req, int32_t advanced, void* q_out, void* hh, int32_t* ret_pos,
+                            int32_t* ret_cnt, int32_t ret_cap, int32_t* dev_status, void* stream);
+
+/* Bytes of workspace sa_paged_decode needs (host function; reads the device's SM count). The workspace is
+ * zero-filled once before its first use (sa_decode_workspace_init does this); every call leaves its counters
+ * at zero again. Calls, and captured graphs, that share a workspace must be ordered on one stream. */
+size_t sa_paged_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim);
+
+/*
+ * sa_paged_decode -- exact softmax attention of one new token per request (the
+ * last of its seq_lens[b] cached ones) over the paged cache.
+ *
+ * The query at position i = seq_lens[b] - 1 sees position j iff
+ *   j <= i and (window == 0 or j > i - window or j < n_sink):
+ * the whole cache, or the `window` most recent tokens, itself included, and the
+ * n_sink first ones. An empty request gives out = 0, lse = -inf.
+ *   q, out   [batch, num_q_heads, head_dim], dtype; 16-byte aligned
+ *   scale    <= 0 selects head_dim ** -0.5
+ *   lse      nullable float32 [batch, num_q_heads], natural log
+ * Tokens that the query does not see are never used, whatever they hold. Pages
+ * whose block id is out of range are skipped with SA_DEV_BAD_BLOCK; a request
+ * longer than its table row is read up to the row's end with SA_DEV_OVERFLOW; a
+ * negative length counts as 0 with SA_DEV_BAD_COUNT. Results do not depend on
+ * timing: repeated calls give the same bits. Limits: batch <= 1024, num_q_heads /
+ * num_kv_heads <= 16.
+ */
+sa_status sa_paged_decode(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
+                          int32_t window, int32_t n_sink, float scale, void* out, float* lse, void* workspace,
+                          size_t workspace_bytes, int32_t* dev_status, void* stream);
+
+/* Bytes of workspace sa_paged_prefill needs for num_tokens rows of q; rules as sa_paged_decode_workspace_size. */
+size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
+                                       int32_t num_tokens);
+
+/*
+ * sa_paged_prefill -- exact causal softmax attention of new tokens over the
+ * paged cache that already holds them (sa_append_kv or sa_append_kv_rope first).
+ *
+ * Request b's queries are rows new_cu[b] .. new_cu[b+1]-1 of q, at positions
+ * seq_lens[b] - n_b .. seq_lens[b] - 1; each sees what sa_paged_decode's query
+ * at its position sees. Prompts, chunks of prompts and a few drafted tokens.
+ *   q, out   [num_tokens, num_q_heads, head_dim], dtype; 16-byte aligned; rows
+ *            from new_cu[batch] on are padding: neither read nor written
+ *   new_cu   [batch + 1] int32, device, non-decreasing, new_cu[0] = 0
+ *   lse      nullable float32 [num_tokens, num_q_heads], natural log
+ * A request whose rows leave [0, num_tokens] sets SA_DEV_BAD_COUNT and is
+ * skipped; one with more new tokens than its length sets SA_DEV_BAD_COUNT, and
+ * its queries before position 0 give out = 0, lse = -inf. Other data errors as
+ * sa_paged_decode. A value row that some query sees and another does not must
+ * be finite (its weight 0 still multiplies it). Limits: num_q_heads /
+ * num_kv_heads <= 16.
+ */
+sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
+                           const int32_t* new_cu, int32_t num_tokens, int32_t window, int32_t n_sink, float scale,
+                           void* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                           void* stream);
+
 /*
  * Self-test of the bounded in-kernel wait (no counterpart on the pages: it
  * checks this library's "Bad data" contract -- every wait inside a kernel
@@ -613,8 +728,9 @@ const char* sa_status_string(sa_status status);
 /* Library version, e.g. "0.1.0" (static string). */
 const char* sa_version(void);
 
-/* sizeof(sa_cache) (which = 0) or sizeof(sa_batch) (which = 1) as built, so a
- * binding can check its struct layout (host function; 0 for other values). */
+/* sizeof(sa_cache) (which = 0), sizeof(sa_batch) (which = 1) or sizeof(sa_rope)
+ * (which = 2) as built, so a binding can check its struct layout (host function;
+ * 0 for other values). */
 size_t sa_struct_size(int32_t which);
 
 #ifdef __cplusplus

@@ -17,6 +17,7 @@ c_size = ctypes.c_size_t
 
 SA_BF16, SA_FP16 = 0, 1
 SA_DEV_BAD_BLOCK, SA_DEV_OVERFLOW, SA_DEV_BAD_COUNT, SA_DEV_TIMEOUT = 1, 2, 4, 8
+SA_DEV_BAD_POSITION = 16
 
 
 class SaCache(ctypes.Structure):
@@ -30,8 +31,16 @@ class SaBatch(ctypes.Structure):
                 ("bt_stride", c_i32)]
 
 
+class SaRope(ctypes.Structure):
+    _fields_ = [("table", c_ptr), ("positions", c_ptr), ("q_weight", c_ptr), ("k_weight", c_ptr),
+                ("max_pos", c_i32), ("rot_dim", c_i32), ("interleaved", c_i32), ("num_axes", c_i32),
+                ("sections", c_i32 * 4), ("eps", c_f32)]
+
+
 P_CACHE = ctypes.POINTER(SaCache)
 P_BATCH = ctypes.POINTER(SaBatch)
+P_ROPE = ctypes.POINTER(SaRope)
+c_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes), as declared in include/sparse_attn.h
 SIGNATURES = {
@@ -78,6 +87,15 @@ SIGNATURES = {
     "sa_shard_selection": (c_i32, [c_ptr, c_ptr, c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_i32, c_ptr,
                                    c_ptr]),
     "sa_merge_states": (c_i32, [c_ptr, c_ptr, c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr]),
+    "sa_append_kv_rope": (c_i32, [P_CACHE, P_BATCH, P_ROPE, c_ptr, c_i64, c_i32, c_ptr, c_i64, c_ptr,
+                                  c_i64, c_ptr, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_ptr,
+                                  c_i32, c_ptr, c_ptr]),
+    "sa_paged_decode_workspace_size": (c_size, [c_i32, c_i32, c_i32, c_i32]),
+    "sa_paged_decode": (c_i32, [P_CACHE, P_BATCH, c_ptr, c_i32, c_i32, c_i32, c_f32, c_ptr, c_ptr,
+                                c_ptr, c_size, c_ptr, c_ptr]),
+    "sa_paged_prefill_workspace_size": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32]),
+    "sa_paged_prefill": (c_i32, [P_CACHE, P_BATCH, c_ptr, c_i32, c_ptr, c_i32, c_i32, c_i32, c_f32,
+                                 c_ptr, c_ptr, c_ptr, c_size, c_ptr, c_ptr]),
     "sa_struct_size": (c_size, [c_i32]),
     "sa_wait_selftest": (c_i32, [c_i32, ctypes.c_int64, c_ptr, c_ptr, c_ptr]),
     "sa_status_string": (ctypes.c_char_p, [c_i32]),

@@ -13,7 +13,7 @@ from typing import Optional
 import torch
 
 from . import _lib
-from ._lib import SaBatch, SaCache
+from ._lib import SaBatch, SaCache, SaRope
 
 __all__ = ["SaError", "SaCache", "SaBatch", "make_cache", "make_batch", "PagedKVCache",
            "sa_append_kv", "sa_score_pages", "sa_select_topk", "sa_decode_workspace_size",
@@ -23,7 +23,9 @@ __all__ = ["SaError", "SaCache", "SaBatch", "make_cache", "make_batch", "PagedKV
            "sa_sparse_decode_qh", "sa_h2o_prefill", "sa_entmax_workspace_size",
            "alloc_entmax_workspace", "sa_sparse_decode_entmax", "sa_sparse_decode_entmax_qh",
            "sa_gauss_select", "sa_shard_lengths", "sa_shard_selection", "sa_merge_states",
-           "batch_view",
+           "batch_view", "SaRope", "make_rope", "rope_table", "sa_append_kv_rope",
+           "sa_paged_decode_workspace_size", "alloc_paged_decode_workspace", "sa_paged_decode",
+           "sa_paged_prefill_workspace_size", "alloc_paged_prefill_workspace", "sa_paged_prefill",
            "sa_status_string", "sa_struct_size", "sa_wait_selftest",
            "sa_version", "alloc_decode_workspace"]
 
@@ -110,7 +112,7 @@ def sa_status_string(status: int) -> str:
 
 
 def sa_struct_size(which: int) -> int:
-    """sizeof(sa_cache) (0) or sizeof(sa_batch) (1) as the library was built."""
+    """sizeof(sa_cache) (0), sizeof(sa_batch) (1) or sizeof(sa_rope) (2) as the library was built."""
     return int(_lib.load().sa_struct_size(int(which)))
 
 
@@ -406,3 +408,165 @@ def sa_h2o_prefill(cache: SaCache, batch: SaBatch, new_cu, hh, num_slots: int, r
         float(decay), float(scale), _p(evicted, torch.int32, "evicted"),
         _p(evicted_cnt, torch.int32, "evicted_cnt"), int(ev_cap),
         _p(dev_status, torch.int32, "dev_status"), _s(stream)))
+
+
+# ---------------------------------------------------------------------------
+# whole layers: rotated append, attention over the whole cache
+# ---------------------------------------------------------------------------
+def rope_table(max_pos: int, rot_dim: int, theta: float = 10000.0, device="cuda") -> torch.Tensor:
+    """Angles of positions 0 .. max_pos - 1, float32 [max_pos, rot_dim]: the cosines of the rot_dim / 2
+    pairs, then their sines, pair i turning by theta ** (-2 i / rot_dim) a position (computed in float64)."""
+    freq = theta ** (-torch.arange(0, rot_dim, 2, dtype=torch.float64, device=device) / rot_dim)
+    angle = torch.arange(max_pos, dtype=torch.float64, device=device)[:, None] * freq
+    return torch.cat([angle.cos(), angle.sin()], 1).float()
+
+
+def make_rope(table: Optional[torch.Tensor], *, interleaved: bool = False,
+              positions: Optional[torch.Tensor] = None, sections=None,
+              q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+              eps: float = 1e-6) -> SaRope:
+    """Struct view of a rotation and its norms: table float32 [max_pos, rot_dim] (None: norms alone),
+    positions int32 [T] or [axes, T] (None: places in the sequence), sections the pairs of each axis,
+    q_weight / k_weight [D] in the cache dtype."""
+    if table is not None and table.dim() != 2:
+        raise ValueError("table must be [max_pos, rot_dim]")
+    max_pos, rot_dim = table.shape if table is not None else (0, 0)
+    axes = 1 if positions is None or positions.dim() == 1 else positions.shape[0]
+    sections = list(sections) if sections is not None else [rot_dim // 2]
+    if not 1 <= axes <= 4 or len(sections) != axes:
+        raise ValueError("sections must name one count of pairs for each of 1 to 4 axes of positions")
+    r = SaRope(_p(table, torch.float32, "table"), _p(positions, torch.int32, "positions"),
+               _p(q_weight, tuple(_DT), "q_weight"), _p(k_weight, tuple(_DT), "k_weight"), max_pos, rot_dim,
+               int(interleaved), axes, (_lib.c_i32 * 4)(*sections), float(eps))
+    r._keep = (table, positions, q_weight, k_weight)
+    return r
+
+
+def _rows(t, name: str, dtype, heads: Optional[int], head_dim: int):
+    """Address and token stride of rows [T, heads, head_dim] whose tokens may lie apart."""
+    if not t.is_cuda or t.dtype != dtype:
+        raise ValueError(f"{name} must be a CUDA tensor of the cache dtype {dtype}")
+    shape, (stride, head, one) = t.shape, t.stride()
+    if shape[2] != head_dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} must be [T, {heads or 'heads'}, {head_dim}], got {tuple(shape)}")
+    if one != 1 or (head != head_dim and shape[1] > 1):
+        raise ValueError(f"the heads of a token of {name} must be contiguous")
+    return t.data_ptr(), stride if shape[0] > 1 else max(stride, shape[1] * head_dim)
+
+
+def _launch(fn_name: str, device, stream, args):
+    """Call `fn_name(*args, stream)` with `device` current, on its current stream unless one is given."""
+    fn = getattr(_lib.load(), fn_name)
+    dev = device.index
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    else:
+        s = stream if isinstance(stream, int) else stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        st = fn(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, s)
+    if st != 0:
+        raise SaError(fn_name, st)
+
+
+def sa_append_kv_rope(cache: SaCache, batch: SaBatch, rope: SaRope, q, k_new, v_new, new_cu,
+                      max_new_per_req: int, q_out, advanced: bool = False, hh=None, ret_pos=None,
+                      ret_cnt=None, ret_cap: int = 0, dev_status=None, stream=None):
+    """Norm and rotation of q [T, H_q, D] (into q_out; both may be None) and k_new [T, H_kv, D], then the
+    append of k_new and v_new. Tokens may lie apart (slices of one projection's output). advanced: the
+    batch's lengths already count the new tokens and stay as they are."""
+    pool = cache._keep[0]
+    dt, H, D = pool.dtype, pool.shape[1], pool.shape[3]
+    T = k_new.shape[0]
+    kp, ks = _rows(k_new, "k_new", dt, H, D)
+    vp, vs = _rows(v_new, "v_new", dt, H, D)
+    qp = qop = None
+    qs = hq = 0
+    if q is not None:
+        qp, qs = _rows(q, "q", dt, None, D)
+        hq = q.shape[1]
+        if q_out is None or q_out.shape != q.shape or q_out.dtype != dt:
+            raise ValueError("q_out must be like q")
+        qop = _p(q_out, name="q_out")
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    if v_new.shape[0] != T or (q is not None and q.shape[0] != T):
+        raise ValueError("q, k_new and v_new must have the same tokens")
+    if new_cu.numel() != batch.batch + 1:
+        raise ValueError("new_cu must be [batch + 1]")
+    positions, qw, kw = rope._keep[1:]
+    if positions is not None and positions.shape[-1] != T:
+        raise ValueError("positions must have one column for each row of k_new")
+    for w in (qw, kw):
+        if w is not None and (w.dtype != dt or w.numel() != D):
+            raise ValueError("q_weight and k_weight must be [head_dim] in the cache dtype")
+    _launch("sa_append_kv_rope", pool.device, stream,
+            (cache, batch, rope, qp, qs, hq, kp, ks, vp, vs, _p(new_cu, torch.int32, "new_cu"), T,
+             max_new_per_req, int(advanced), qop, _p(hh, torch.bfloat16, "hh"),
+             _p(ret_pos, torch.int32, "ret_pos"), _p(ret_cnt, torch.int32, "ret_cnt"), ret_cap,
+             _p(dev_status, torch.int32, "dev_status")))
+
+
+def sa_paged_decode_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int, head_dim: int) -> int:
+    return int(_lib.load().sa_paged_decode_workspace_size(int(batch), int(num_kv_heads), int(num_q_heads),
+                                                          int(head_dim)))
+
+
+def alloc_paged_decode_workspace(batch, num_kv_heads, num_q_heads, head_dim, device="cuda"):
+    """A zero-filled workspace tensor of the size sa_paged_decode needs."""
+    with torch.cuda.device(device):
+        n = max(256, sa_paged_decode_workspace_size(batch, num_kv_heads, num_q_heads, head_dim))
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def sa_paged_prefill_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int, head_dim: int,
+                                    num_tokens: int) -> int:
+    return int(_lib.load().sa_paged_prefill_workspace_size(int(batch), int(num_kv_heads), int(num_q_heads),
+                                                           int(head_dim), int(num_tokens)))
+
+
+def alloc_paged_prefill_workspace(batch, num_kv_heads, num_q_heads, head_dim, num_tokens, device="cuda"):
+    """A zero-filled workspace tensor of the size sa_paged_prefill needs for up to num_tokens rows."""
+    with torch.cuda.device(device):
+        n = max(256, sa_paged_prefill_workspace_size(batch, num_kv_heads, num_q_heads, head_dim, num_tokens))
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def _attention(cache, q, num_q_heads, out, lse, workspace):
+    """Addresses of the rows of an attention call, checked: q, out, lse, workspace and its bytes."""
+    pool = cache._keep[0]
+    dt = pool.dtype
+    if q.dim() != 3 or q.shape[1] != num_q_heads or q.shape[2] != pool.shape[3]:
+        raise ValueError(f"q must be [rows, {num_q_heads}, {pool.shape[3]}], got {tuple(q.shape)}")
+    if out.shape != q.shape:
+        raise ValueError("out must be like q")
+    if lse is not None and lse.shape != q.shape[:2]:
+        raise ValueError("lse must be [rows, num_q_heads]")
+    return (_p(q, dt, "q"), _p(out, dt, "out"), _p(lse, torch.float32, "lse"), _p(workspace, name="workspace"),
+            0 if workspace is None else workspace.numel() * workspace.element_size(), pool.device)
+
+
+def sa_paged_decode(cache: SaCache, batch: SaBatch, q, num_q_heads: int, scale: float, out, window: int = 0,
+                    n_sink: int = 0, lse=None, workspace=None, dev_status=None, stream=None):
+    """Attention of one new token per request, q [B, H_q, D], over its whole cache (window 0), or the
+    `window` most recent tokens and the n_sink first ones."""
+    qp, op, lp, wp, wbytes, device = _attention(cache, q, num_q_heads, out, lse, workspace)
+    if q.shape[0] != batch.batch:
+        raise ValueError("q must have one row for each request")
+    _launch("sa_paged_decode", device, stream,
+            (cache, batch, qp, num_q_heads, window, n_sink, scale, op, lp, wp, wbytes,
+             _p(dev_status, torch.int32, "dev_status")))
+
+
+def sa_paged_prefill(cache: SaCache, batch: SaBatch, q, num_q_heads: int, new_cu, scale: float, out,
+                     window: int = 0, n_sink: int = 0, lse=None, workspace=None, dev_status=None, stream=None):
+    """Causal attention of the new tokens q [T, H_q, D] (request b's rows new_cu[b] .. new_cu[b + 1] - 1,
+    already appended) over the cache, with sa_paged_decode's window."""
+    qp, op, lp, wp, wbytes, device = _attention(cache, q, num_q_heads, out, lse, workspace)
+    if new_cu.numel() != batch.batch + 1:
+        raise ValueError("new_cu must be [batch + 1]")
+    _launch("sa_paged_prefill", device, stream,
+            (cache, batch, qp, num_q_heads, _p(new_cu, torch.int32, "new_cu"), q.shape[0], window, n_sink, scale,
+             op, lp, wp, wbytes, _p(dev_status, torch.int32, "dev_status")))

@@ -31,10 +31,9 @@
 // last CTA of the unit to finish (atomic ticket) merges the partials exactly,
 // writes out / lse and resets the ticket. No CTA waits on another; every
 // mbarrier wait is time-bounded.
-#include <cuda.h>
-
 #include "common.cuh"
 #include "host.h"
+#include "tma_map.h"
 
 namespace sa {
 namespace {
@@ -655,41 +654,6 @@ WsLayout ws_layout(int units, int G, int D, int nsplit) {
   return w;
 }
 
-// cuTensorMapEncodeTiled through the runtime's driver entry point (no libcuda link).
-using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
-                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*,
-                              CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion,
-                              CUtensorMapFloatOOBfill);
-EncodeFn encode_fn() {
-  static EncodeFn fn = nullptr;
-  static bool tried = false;
-  if (!tried) {
-    tried = true;
-    void* p = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) ==
-            cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeFn>(p);
-  }
-  return fn;
-}
-
-// Tensor map over every pool row: [rows = num_blocks * H * page_size, D], box 16 x 64, 128-byte swizzle.
-bool make_pool_map(CUtensorMap* m, const void* base, const sa_cache* c) {
-  EncodeFn fn = encode_fn();
-  if (!fn) return false;
-  const cuuint64_t rows = cuuint64_t(c->num_blocks) * c->num_kv_heads * c->page_size;
-  if (rows >= (cuuint64_t(1) << 31)) return false;
-  const cuuint64_t dims[2] = {cuuint64_t(c->head_dim), rows};
-  const cuuint64_t strides[1] = {cuuint64_t(c->head_dim) * 2};
-  const cuuint32_t box[2] = {64, 16};
-  const cuuint32_t estr[2] = {1, 1};
-  return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, const_cast<void*>(base), dims, strides, box, estr,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
 int g_dec_smem[16][64];
 
 template <typename T, int D, bool kTma, bool kCluster>
@@ -723,7 +687,7 @@ template <typename T, int D>
 sa_status dispatch_tma(const DecodeArgs& a, dim3 grid, cudaStream_t s, const sa_cache* c, int slot,
                        bool allow_cluster, bool pdl) {
   CUtensorMap mk, mv;
-  if (c->page_size >= 16 && make_pool_map(&mk, c->k, c) && make_pool_map(&mv, c->v, c))
+  if (c->page_size >= 16 && make_pool_map(&mk, c->k, c, 16) && make_pool_map(&mv, c->v, c, 16))
     return launch_merge_mode<T, D, true>(a, grid, s, mk, mv, slot, allow_cluster, pdl);
   memset(&mk, 0, sizeof(mk));
   memset(&mv, 0, sizeof(mv));

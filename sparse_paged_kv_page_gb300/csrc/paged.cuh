@@ -1,0 +1,66 @@
+// Pieces shared by the attention kernels over the whole paged cache
+// (sa_paged_decode, sa_paged_prefill): the visible range of a query, shared-memory
+// tiles of 16 rows, and the search for a work item's request.
+#pragma once
+
+#include "common.cuh"
+
+namespace sa {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+
+// Tiles of R positions that queries at positions [first, last] see of a cache of
+// `len` readable tokens: the n_sink first ones and the `window` most recent ones
+// (window <= 0: all). Tile t < sink_tiles is tile t of the sequence, the others
+// continue at win_tile; the two ranges are disjoint.
+template <int R>
+struct Span {
+  int sink_tiles, win_tile, tiles;
+  __device__ __forceinline__ Span(int first, int last, int len, int window, int n_sink) {
+    const int end = max(0, min(last + 1, len));
+    const int w0 = window > 0 ? max(0, min(first - window + 1, end)) : 0;
+    sink_tiles = (min(n_sink, w0) + R - 1) / R;
+    win_tile = w0 / R;
+    if (win_tile <= sink_tiles) sink_tiles = win_tile = 0;
+    tiles = sink_tiles + (end + R - 1) / R - win_tile;
+  }
+  __device__ __forceinline__ int start(int t) const { return (t < sink_tiles ? t : t - sink_tiles + win_tile) * R; }
+};
+
+// 16 rows x D columns of 2-byte elements in shared memory: 64-column halves of
+// 16 x 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7), the TMA engine's
+// 128-byte swizzle.
+template <int D>
+__device__ __forceinline__ uint32_t swz16(int row, int chunk) {
+  return uint32_t((chunk >> 3) * 2048 + row * 128 + (((chunk & 7) ^ (row & 7)) << 4));
+}
+
+// Work item `idx` of a ragged batch in which request b has ceil(n_b / per) items
+// (n_b = new_cu[b+1] - new_cu[b]): its request and its place there. All lanes of
+// a warp call it. False behind the last item.
+__device__ __forceinline__ bool find_item(const int32_t* new_cu, int batch, int per, int idx, int& b, int& i) {
+  const int lane = threadIdx.x & 31;
+  int before = 0;
+  for (int b0 = 0; b0 < batch; b0 += 32) {
+    const bool in = b0 + lane < batch;
+    const int n = in ? new_cu[b0 + lane + 1] - new_cu[b0 + lane] : 0;
+    const int items = n > 0 ? (n + per - 1) / per : 0;
+    int x = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(kFull, x, o);
+      if (lane >= o) x += y;
+    }
+    const int k = __popc(__ballot_sync(kFull, before + x <= idx));
+    if (k < 32) {
+      i = idx - before - (__shfl_sync(kFull, x, k) - __shfl_sync(kFull, items, k));
+      b = b0 + k;
+      return true;
+    }
+    before += __shfl_sync(kFull, x, 31);
+  }
+  return false;
+}
+
+}  // namespace sa
