@@ -1,198 +1,570 @@
 // sa_paged_prefill: causal softmax attention of new tokens (a prompt, a chunk of
 // one, a few drafted tokens) over the paged cache that already holds them.
+//
+// Mathematics: o = sum_j p_j v_j, p = softmax(scale q . k_j) over the visible
+// positions j, in one pass with a running maximum m and sum l. O is rescaled only
+// where m has grown by more than 2^8 since it was last used (p stays below 2^8,
+// exact in float32 sums and inside both 16-bit types); the quotient o / l at the
+// end makes any m right.
+//
+// A CTA owns 2 x 128 packed rows (token, query head of one KV head's group), so a
+// key is read once for all G heads, and walks the visible keys 128 at a time. The
+// products run on the 5th-generation tensor cores, accumulators in TMEM: S = Q K^T
+// (128 x 128, one per half), P over S's columns as the A operand from TMEM, O += P V.
+// Two warpgroups take the two halves, one row a thread (no shuffles): while one
+// turns S into P the tensor cores work for the other. One warp issues the products,
+// one the copies: keys and values in a ring of 128-row slots, page by page through
+// a tensor map (pages of 8 tokens and more), or row by row with cp.async (smaller
+// pages, and tiles with rows that must not be read: those get zeros).
+//
+// Bound by the tensor cores for prompts; for a few rows over a long cache by HBM,
+// where the keys are split over CTAs and the last of an item's CTAs merges the
+// parts in order.
+#include <type_traits>
+
 #include "common.cuh"
 #include "host.h"
 #include "paged.cuh"
+#include "tc5.cuh"
+#include "tma_map.h"
 
 namespace sa {
 namespace {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = kWarps * 32;
-constexpr int kRows = 16 * kWarps;      // packed rows (token, query head of the group) of a CTA
-constexpr int kKeys = 32;               // positions per step
+constexpr int kKeys = 128;                // positions per step
+constexpr int kMmaWarp = 8;               // warps 0-3 and 4-7: the softmax of the two halves
+constexpr int kSoftmaxThreads = 32 * kMmaWarp;
+constexpr int kThreads = kSoftmaxThreads + 128;
+// Registers: 384 threads are launched with 168 each; the softmax warpgroups take
+// 208 (a row of 128 scores a thread) of what the third one gives back:
+// 256 x 208 + 128 x 88 = 384 x 168.
+constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
+constexpr int kTileRing = 8;              // steps whose row masks are kept
+constexpr float kGrow = 8.0f;             // log2 of the growth of the maximum that O does not follow
+constexpr int kMaxSplit = 64;
 
 struct PagedPrefillArgs {
   const void* k;
   const void* v;
-  const void* q;
   const int32_t* bt;
   const int32_t* seq_lens;
   const int32_t* new_cu;
   void* out;
   float* lse;
+  float* part_o;        // [items * H_kv][splits][256][D]
+  float* part_lse;      // [items * H_kv][splits][256]
+  int32_t* tickets;     // [items * H_kv]
   int32_t* status;
-  int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink;
+  int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink, items;
   float scale_log2;
 };
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kThreads) paged_prefill_kernel(const __grid_constant__ PagedPrefillArgs a) {
-  using E = Elem<T>;
-  constexpr int kTileBytes = 16 * D * 2;
-  __shared__ __align__(1024) uint8_t s_kv[2][2][kKeys / 16][kTileBytes];   // [stage][K, V][tile]
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, tq = lane & 3;
-  const int G = a.G, per = kRows / G, pss = a.ps_shift;
-  const int h = blockIdx.x % a.H_kv, idx = gridDim.x / a.H_kv - 1 - blockIdx.x / a.H_kv;
-  int b, item;
-  if (!find_item(a.new_cu, a.batch, per, idx, b, item)) return;
-  const int c0 = a.new_cu[b], n = a.new_cu[b + 1] - c0, L = a.seq_lens[b];
-  const int cap = int(min(int64_t(a.bt_stride) << pss, int64_t(0x7fffffff)));
-  if (threadIdx.x == 0 && item == 0 && h == 0) {
-    if (c0 < 0 || c0 + n > a.T || L < n) flag(a.status, SA_DEV_BAD_COUNT);
-    if (L > cap) flag(a.status, SA_DEV_OVERFLOW);
-  }
-  if (c0 < 0 || int64_t(c0) + n > a.T) return;
-  const int t0 = item * per, nt = min(per, n - t0);           // tokens of this CTA
-  const int first = L - n + t0, last = first + nt - 1;        // their positions
-  const int len = min(max(L, 0), cap);
-  const Span<kKeys> sp(first, last, len, a.window, a.n_sink);
+template <int D, bool kTma>
+struct Cfg {
+  static constexpr int kProducers = kTma ? 1 : 3;                  // copy warps
+  static constexpr int kHalves = D / 64;                           // 64-column halves of a row
+  static constexpr int kSlotBytes = kHalves * kKeys * 128;
+  static constexpr int kSlots = D == 128 ? 5 : 8;
+  static constexpr int kQBytes = 2 * kSlotBytes;
+  static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + 1024;
+};
 
-  // rows of this thread: r0 = warp * 16 + g and r0 + 8
-  int pos[2];
-  int64_t row[2];
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    const int x = warp * 16 + g + 8 * r, t = x / G;
-    const bool in = t < nt;
-    pos[r] = in ? first + t : -1;
-    row[r] = in ? (int64_t(c0 + t0 + t) * a.H_q + int64_t(h) * G + x % G) : -1;
-  }
-  uint32_t qa[D / 16][4];
-#pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    const int x0 = (kk * 16 + 2 * tq) >> 1;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      const uint32_t* qp = static_cast<const uint32_t*>(a.q) + row[r] * (D / 2);
-      qa[kk][r] = row[r] >= 0 ? qp[x0] : 0u;
-      qa[kk][2 + r] = row[r] >= 0 ? qp[x0 + 4] : 0u;
+struct Shared {
+  uint64_t full[8], empty[8], q, s[2], p[2], o[2];
+  uint32_t tile[kTileRing][1 + kKeys / 32];   // [0]: rows of the step are masked by the words that follow
+  int64_t off[kKeys];                         // pool row of each position of a gathered step, -1: none
+  uint32_t tmem;
+  int abort, last;
+};
+
+// Wait for a phase; false once any wait of the CTA has given up.
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared& sh, int32_t* status) {
+  const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return true;
+  const uint64_t t0 = global_ns();
+  while (true) {
+#pragma unroll 1
+    for (int i = 0; i < 64; ++i)
+      if (mbar_try_wait(b, parity)) return true;
+    if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
+    if (global_ns() - t0 > kWaitLimitNs) {
+      flag(status, SA_DEV_TIMEOUT);
+      *reinterpret_cast<volatile int*>(&sh.abort) = 1;
+      return false;
     }
-  }
-  const int32_t* btb = a.bt + int64_t(b) * a.bt_stride;
-  __shared__ uint32_t s_ok[2][kThreads / 32];
-  // copies of step i: thread (row, part) -> 16-byte chunks of one K and V row
-  constexpr int kParts = kThreads / kKeys;
-  auto issue = [&](int i) {
-    if (i < sp.tiles) {
-      const int r = threadIdx.x % kKeys, part = threadIdx.x / kKeys, j = sp.start(i) + r;
-      int blk = -1;
-      // rows that no query of the CTA sees could hold anything (NaN): zeros instead
-      if (j < len && j <= last && (a.window == 0 || j > first - a.window || j < a.n_sink)) {
-        blk = btb[j >> pss];
-        if (blk < 0 || blk >= a.num_blocks) {
-          flag(a.status, SA_DEV_BAD_BLOCK);
-          blk = -1;
-        }
-      }
-      if (part == 0) s_ok[i & 1][0] = __ballot_sync(kFull, blk >= 0);
-      const int64_t off = (((int64_t(blk) * a.H_kv + h) << pss) + (j & ((1 << pss) - 1))) * D;
-      const uint32_t sk = smem_u32(&s_kv[i & 1][0][r >> 4][0]), sv = smem_u32(&s_kv[i & 1][1][r >> 4][0]);
-#pragma unroll
-      for (int c = part; c < D / 8; c += kParts) {
-        const uint32_t d = swz16<D>(r & 15, c);
-        cp_async_16(sk + d, blk >= 0 ? static_cast<const T*>(a.k) + off + c * 8 : a.k, blk >= 0 ? 16 : 0);
-        cp_async_16(sv + d, blk >= 0 ? static_cast<const T*>(a.v) + off + c * 8 : a.v, blk >= 0 ? 16 : 0);
-      }
-    }
-    cp_async_commit();
-  };
-  float o[D / 8][4];
-#pragma unroll
-  for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-  float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
-  issue(0);
-  for (int i = 0; i < sp.tiles; ++i) {
-    issue(i + 1);
-    cp_async_wait<1>();
-    __syncthreads();
-    const uint32_t okm = s_ok[i & 1][0];
-    const int j0 = sp.start(i);
-    const int mi = lane >> 3, rr = lane & 7;
-    float c[kKeys / 8][4];
-#pragma unroll
-    for (int x = 0; x < kKeys / 8; ++x) c[x][0] = c[x][1] = c[x][2] = c[x][3] = 0.f;
-#pragma unroll
-    for (int t = 0; t < kKeys / 16; ++t) {
-      const uint32_t sk = smem_u32(&s_kv[i & 1][0][t][0]);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        uint32_t r[4];
-        ldmatrix_x4(r, sk + swz16<D>((mi >> 1) * 8 + rr, kk * 2 + (mi & 1)));
-        E::mma(c[2 * t], qa[kk], r[0], r[1]);
-        E::mma(c[2 * t + 1], qa[kk], r[2], r[3]);
-      }
-    }
-    float pmax[2] = {-INFINITY, -INFINITY};
-#pragma unroll
-    for (int x = 0; x < kKeys / 8; ++x) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int jj = x * 8 + 2 * tq + (e & 1), j = j0 + jj, r = e >> 1;
-        const bool ok = ((okm >> jj) & 1u) && j <= pos[r] &&
-                        (a.window == 0 || j > pos[r] - a.window || j < a.n_sink);
-        c[x][e] = ok ? c[x][e] * a.scale_log2 : -INFINITY;
-        pmax[r] = fmaxf(pmax[r], c[x][e]);
-      }
-    }
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      pmax[r] = fmaxf(pmax[r], __shfl_xor_sync(kFull, pmax[r], 1));
-      pmax[r] = fmaxf(pmax[r], __shfl_xor_sync(kFull, pmax[r], 2));
-      const float m_new = fmaxf(m_r[r], pmax[r]);
-      const float m_use = m_new == -INFINITY ? 0.f : m_new;
-      const float alpha = ex2_approx(m_r[r] - m_use);
-      float rs = 0.f;
-#pragma unroll
-      for (int x = 0; x < kKeys / 8; ++x) {
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          const float p = ex2_approx(c[x][2 * r + e] - m_use);
-          c[x][2 * r + e] = p;
-          rs += p;
-        }
-      }
-      l_r[r] = l_r[r] * alpha + rs;
-      m_r[r] = m_new;
-#pragma unroll
-      for (int x = 0; x < D / 8; ++x) {
-        o[x][2 * r] *= alpha;
-        o[x][2 * r + 1] *= alpha;
-      }
-    }
-#pragma unroll
-    for (int t = 0; t < kKeys / 16; ++t) {
-      const uint32_t sv = smem_u32(&s_kv[i & 1][1][t][0]);
-      const uint32_t pa[4] = {E::pack(c[2 * t][0], c[2 * t][1]), E::pack(c[2 * t][2], c[2 * t][3]),
-                              E::pack(c[2 * t + 1][0], c[2 * t + 1][1]), E::pack(c[2 * t + 1][2], c[2 * t + 1][3])};
-#pragma unroll
-      for (int nd = 0; nd < D / 16; ++nd) {
-        uint32_t r[4];
-        ldmatrix_x4_trans(r, sv + swz16<D>((mi & 1) * 8 + rr, 2 * nd + (mi >> 1)));
-        E::mma(o[2 * nd], pa, r[0], r[1]);
-        E::mma(o[2 * nd + 1], pa, r[2], r[3]);
-      }
-    }
-    __syncthreads();
-  }
-  cp_async_wait<0>();
-#pragma unroll
-  for (int r = 0; r < 2; ++r) {
-    l_r[r] += __shfl_xor_sync(kFull, l_r[r], 1);
-    l_r[r] += __shfl_xor_sync(kFull, l_r[r], 2);
-    if (row[r] < 0) continue;
-    const float inv = l_r[r] > 0.f ? 1.0f / l_r[r] : 0.f;
-    uint32_t* op = static_cast<uint32_t*>(a.out) + row[r] * (D / 2);
-#pragma unroll
-    for (int x = 0; x < D / 8; ++x) op[x * 4 + tq] = E::pack(o[x][2 * r] * inv, o[x][2 * r + 1] * inv);
-    if (a.lse && tq == 0) a.lse[row[r]] = l_r[r] > 0.f ? (m_r[r] + lg2_approx(l_r[r])) * kLn2 : -INFINITY;
   }
 }
 
+template <typename T, int D, bool kTma>
+__global__ void __launch_bounds__(kThreads, 1)
+    paged_prefill_kernel(const __grid_constant__ PagedPrefillArgs a, const __grid_constant__ CUtensorMap tmq,
+                         const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
+  using E = Elem<T>;
+  using C = Cfg<D, kTma>;
+  constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+  extern __shared__ __align__(128) uint8_t smem_raw[];
+  __shared__ Shared sh;
+  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  uint8_t* ring = smem + C::kQBytes;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int G = a.G, pss = a.ps_shift, half_tokens = 128 / G;
+
+  // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
+  const int h = blockIdx.x / a.items, idx = a.items - 1 - blockIdx.x % a.items;
+  int b, item;
+  if (!find_item(a.new_cu, a.batch, 2 * half_tokens, idx, b, item)) return;
+  const int c0 = a.new_cu[b], n = a.new_cu[b + 1] - c0, L = a.seq_lens[b];
+  const int cap = int(min(int64_t(a.bt_stride) << pss, int64_t(0x7fffffff)));
+  if (threadIdx.x == 0 && item == 0 && h == 0 && blockIdx.y == 0) {
+    if (c0 < 0 || int64_t(c0) + n > a.T || L < n) flag(a.status, SA_DEV_BAD_COUNT);
+    if (L > cap) flag(a.status, SA_DEV_OVERFLOW);
+  }
+  if (c0 < 0 || int64_t(c0) + n > a.T) return;
+  const int t0 = item * 2 * half_tokens, nt = min(2 * half_tokens, n - t0);
+  const int first = L - n + t0, last = first + nt - 1, len = min(max(L, 0), cap);
+  const Span<kKeys> sp(first, last, len, a.window, a.n_sink);
+  const bool two = nt > half_tokens;                              // the second half has rows
+  const int ns = gridDim.y, per = (sp.tiles + ns - 1) / ns;
+  const int tb = min(sp.tiles, int(blockIdx.y) * per), steps = min(sp.tiles, tb + per) - tb;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::kSlots; ++i) {
+      mbar_init(smem_u32(&sh.full[i]), 1);
+      mbar_init(smem_u32(&sh.empty[i]), 1);
+    }
+    mbar_init(smem_u32(&sh.q), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&sh.s[i]), 1);
+      mbar_init(smem_u32(&sh.p[i]), 4);
+      mbar_init(smem_u32(&sh.o[i]), 1);
+    }
+    mbar_init_fence();
+    sh.abort = 0;
+  }
+  if (warp == kMmaWarp) tc5_alloc(smem_u32(&sh.tmem), 512);
+  tc5_fence_before();
+  __syncthreads();
+  tc5_fence_after();
+  const uint32_t tmem = sh.tmem;                                  // columns: S/P of the halves, then O of the halves
+
+  if (warp < kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+    // ------------------------------------------------------------- softmax: one row a thread
+    const int tile = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = uint32_t(warp & 3) << 21;              // TMEM lane 32 * (warp % 4)
+    const uint32_t s_col = tmem + lanes + tile * 128, o_col = tmem + lanes + 256 + tile * 128;
+    const int t = tile * half_tokens + row / G;
+    const bool in = row / G < half_tokens && t < nt;
+    const int pos = in ? first + t : -1;
+    const int64_t orow = in ? int64_t(c0 + t0 + t) * a.H_q + int64_t(h) * G + row % G : -1;
+    float m = -INFINITY, l = 0.f;
+    const bool act = tile == 0 || two;
+    for (int j = 0; act && j < steps; ++j) {
+      if (!__all_sync(kFull, wait_on(&sh.s[tile], j & 1, sh, a.status))) break;
+      tc5_fence_after();
+      float s[kKeys];
+#pragma unroll
+      for (int c = 0; c < 4; ++c) tc5_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, s_col + 32 * c);
+      const int j0 = sp.start(tb + j);
+      const uint32_t* words = sh.tile[j % kTileRing];
+      const uint32_t masked = *reinterpret_cast<const volatile uint32_t*>(words);
+      // columns seen: up to hi, from lo on or below sk
+      const int hi = min(pos, len - 1) - j0;
+      const int lo = a.window > 0 ? pos - a.window + 1 - j0 : 0, sk = a.n_sink - j0;
+      tc5_wait_ld();
+      if (__any_sync(kFull, hi < kKeys - 1 || (lo > 0 && sk < kKeys) || masked)) {
+#pragma unroll
+        for (int c = 0; c < kKeys; ++c)
+          if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
+        if (masked) {
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t bits = reinterpret_cast<const volatile uint32_t*>(words)[1 + w];
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (!((bits >> c) & 1u)) s[32 * w + c] = -INFINITY;
+          }
+        }
+      }
+      float mx[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+      for (int c = 4; c < kKeys - 4; c += 8) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[c + x], s[c + 4 + x]);
+      }
+#pragma unroll
+      for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[kKeys - 4 + x]);
+      const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+      if (j == 0) {
+        m = m_new;
+      } else if (__any_sync(kFull, (m_new - m) * a.scale_log2 > kGrow)) {
+        // S of this step is complete, so the products into O before it are too
+        const float f = m_new == m ? 1.f : ex2_approx((m - m_new) * a.scale_log2);
+        l *= f;
+        m = m_new;
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          float o[32];
+          tc5_ld32(reinterpret_cast<uint32_t*>(o), o_col + 32 * c);
+          tc5_wait_ld();
+#pragma unroll
+          for (int x = 0; x < 32; ++x) o[x] *= f;
+          tc5_st32(o_col + 32 * c, reinterpret_cast<uint32_t*>(o));
+        }
+      }
+      const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
+      float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t w[16];
+#pragma unroll
+        for (int x = 0; x < 16; ++x) {
+          float p0, p1;
+          fma2(p0, p1, s[32 * c + 2 * x], s[32 * c + 2 * x + 1], a.scale_log2, base);
+          p0 = ex2_approx(p0);
+          p1 = ex2_approx(p1);
+          add2(sum[2 * (x & 1)], sum[2 * (x & 1) + 1], p0, p1);
+          w[x] = E::pack(p0, p1);
+        }
+        tc5_st16(s_col + 16 * c, w);
+      }
+      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      tc5_wait_st();
+      tc5_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&sh.p[tile]));
+    }
+    // ------------------------------------------------------------- outputs
+    if (act) {
+      bool ok = steps == 0 || wait_on(&sh.o[tile], 0, sh, a.status);
+      ok = __all_sync(kFull, ok) && steps > 0;
+      tc5_fence_after();
+      const float inv = l > 0.f ? 1.0f / l : 0.f;
+      const float row_lse = l > 0.f ? (m * a.scale_log2 + lg2_approx(l)) * kLn2 : -INFINITY;
+      const int64_t prow = ((int64_t(blockIdx.x) * ns + blockIdx.y) * 2 + tile) * 128 + row;
+      if (in) {
+        if (ns > 1) a.part_lse[prow] = row_lse;
+        else if (a.lse) a.lse[orow] = row_lse;
+      }
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        float o[32];
+        __syncwarp();
+        if (ok) {
+          tc5_ld32(reinterpret_cast<uint32_t*>(o), o_col + 32 * c);
+          tc5_wait_ld();
+        }
+#pragma unroll
+        for (int x = 0; x < 32; ++x) o[x] = l > 0.f ? o[x] * inv : 0.f;
+        if (in && ns > 1) {
+          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+#pragma unroll
+          for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+        } else if (in) {
+          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + 32 * c);
+#pragma unroll
+          for (int x = 0; x < 4; ++x)
+            dst[x] = make_uint4(E::pack(o[8 * x], o[8 * x + 1]), E::pack(o[8 * x + 2], o[8 * x + 3]),
+                                E::pack(o[8 * x + 4], o[8 * x + 5]), E::pack(o[8 * x + 6], o[8 * x + 7]));
+        }
+      }
+      tc5_fence_before();
+    }
+  } else {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
+  if (warp == kMmaWarp) {
+    // ------------------------------------------------------------- products, issued by one thread
+    if (lane == 0 && steps > 0) {
+      constexpr uint32_t id_s = tc5_idesc(kBf16, 128, kKeys, false), id_o = tc5_idesc(kBf16, 128, D, true);
+      const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+      auto scores = [&](int tile, int slot) {                       // S = Q K^T
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          const uint32_t in_row = (kk >> 2) * (kKeys * 128) + (kk & 3) * 32;
+          tc5_mma_ss(tmem + tile * 128, tc5_desc(q_addr + tile * C::kSlotBytes + in_row, 16, 1024),
+                     tc5_desc(r_addr + slot * C::kSlotBytes + in_row, 16, 1024), id_s, kk > 0);
+        }
+      };
+      auto outputs = [&](int tile, int slot, bool add) {            // O += P V
+#pragma unroll
+        for (int kk = 0; kk < kKeys / 16; ++kk)
+          tc5_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + kk * 8,
+                     tc5_desc(r_addr + slot * C::kSlotBytes + kk * 2048, kKeys * 128, 1024), id_o, add || kk > 0);
+      };
+      auto wait_full = [&](int seq) { return wait_on(&sh.full[seq % C::kSlots], (seq / C::kSlots) & 1, sh, a.status); };
+      bool ok = wait_on(&sh.q, 0, sh, a.status) && wait_full(0);
+      if (ok) {
+        tc5_fence_after();
+        scores(0, 0);
+        tc5_commit(smem_u32(&sh.s[0]));
+        if (two) {
+          scores(1, 0);
+          tc5_commit(smem_u32(&sh.s[1]));
+        }
+        tc5_commit(smem_u32(&sh.empty[0]));
+      }
+      for (int j = 0; ok && j < steps; ++j) {
+        const int sv = 2 * j + 1, sk = 2 * j + 2;
+        const bool more = j + 1 < steps;
+        if (!(ok = wait_full(sv) && wait_on(&sh.p[0], j & 1, sh, a.status))) break;
+        tc5_fence_after();
+        outputs(0, sv % C::kSlots, j > 0);
+        if (!more) tc5_commit(smem_u32(&sh.o[0]));
+        if (more) {
+          if (!(ok = wait_full(sk))) break;
+          tc5_fence_after();
+          scores(0, sk % C::kSlots);
+          tc5_commit(smem_u32(&sh.s[0]));
+        }
+        if (two) {
+          if (!(ok = wait_on(&sh.p[1], j & 1, sh, a.status))) break;
+          tc5_fence_after();
+          outputs(1, sv % C::kSlots, j > 0);
+          if (!more) tc5_commit(smem_u32(&sh.o[1]));
+        }
+        tc5_commit(smem_u32(&sh.empty[sv % C::kSlots]));
+        if (more) {
+          if (two) {
+            scores(1, sk % C::kSlots);
+            tc5_commit(smem_u32(&sh.s[1]));
+          }
+          tc5_commit(smem_u32(&sh.empty[sk % C::kSlots]));
+        }
+      }
+      if (!ok) {                                                    // let what was issued finish
+        tc5_commit(smem_u32(&sh.o[0]));
+        mbar_wait(smem_u32(&sh.o[0]), 0, a.status);
+      }
+    }
+    __syncwarp();
+  } else if (warp <= kMmaWarp + C::kProducers) {
+    // ------------------------------------------------------------- copies
+    constexpr int kCopyThreads = 32 * C::kProducers;
+    const int ct = threadIdx.x - 32 * (kMmaWarp + 1);
+    auto copy_sync = [&]() {
+      if (C::kProducers == 1) __syncwarp();
+      else asm volatile("bar.sync 1, %0;\n" ::"n"(kCopyThreads) : "memory");
+    };
+    const int w0 = a.window > 0 ? max(0, first - a.window + 1) : 0;
+    const int32_t* btb = a.bt + int64_t(b) * a.bt_stride;
+    const int ps = 1 << pss;
+    if (steps > 0 && ct == 0) {
+      const uint32_t bar = smem_u32(&sh.q);
+      mbar_arrive_expect_tx(bar, uint32_t((two ? 2 : 1) * C::kHalves * G * half_tokens * 128));
+      for (int tile = 0; tile < (two ? 2 : 1); ++tile)
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(smem_u32(smem) + tile * C::kSlotBytes + hf * kKeys * 128, &tmq, hf * 64, h * G,
+                      c0 + t0 + tile * half_tokens, bar);
+    }
+    // The block ids of a step through the tensor map, one a lane; -1 where there is none.
+    auto page_ids = [&](int j) {
+      int id = -1;
+      if (kTma && j < steps) {
+        const int at = sp.start(tb + j) + (lane << pss);
+        if (lane < (kKeys >> pss) && at < len) id = btb[at >> pss];
+      }
+      return id;
+    };
+    int pending = -1;                                              // slot whose gathered rows are still under way
+    auto finish = [&](int slot) {
+      fence_proxy_async_smem();
+      copy_sync();
+      if (ct == 0) mbar_arrive(smem_u32(&sh.full[slot]));
+    };
+    int ids = page_ids(0);
+    bool ok = true;
+    int seq = 0;
+    for (int j = 0; ok && j < steps; ++j) {
+      const int j0 = sp.start(tb + j);
+      const int cur = ids;
+      ids = page_ids(j + 1);
+      // every row of the step may be read, and comes from a page that exists
+      bool clean = false;
+      if (kTma) {
+        clean = j0 + kKeys <= len && (j0 >= w0 || j0 + kKeys <= a.n_sink);
+        clean = clean && __all_sync(kFull, lane >= (kKeys >> pss) || (cur >= 0 && cur < a.num_blocks));
+      }
+      if (!clean) {
+        copy_sync();                                               // the offsets of the step before are used up
+        for (int r0 = 0; r0 < kKeys; r0 += kCopyThreads) {
+          const int r = r0 + ct, p = j0 + r;
+          if (r >= kKeys) break;                                   // (whole warps)
+          int64_t off = -1;
+          if (p < len && (p >= w0 || p < a.n_sink)) {
+            const int blk = btb[p >> pss];
+            if (blk < 0 || blk >= a.num_blocks) flag(a.status, SA_DEV_BAD_BLOCK);
+            else off = ((int64_t(blk) * a.H_kv + h) << pss) + (p & (ps - 1));
+          }
+          sh.off[r] = off;
+          const uint32_t bits = __ballot_sync(kFull, off >= 0);
+          if (lane == 0) sh.tile[j % kTileRing][1 + r / 32] = bits;
+        }
+      }
+      if (ct == 0) sh.tile[j % kTileRing][0] = !clean;
+      copy_sync();
+#pragma unroll 1
+      for (int part = 0; part < 2; ++part, ++seq) {
+        const int slot = seq % C::kSlots;
+        if (seq >= C::kSlots) {
+          ok = wait_on(&sh.empty[slot], (seq / C::kSlots - 1) & 1, sh, a.status);
+          ok = __all_sync(kFull, ok);
+          if (!ok) break;
+        }
+        const uint32_t dst = smem_u32(ring) + slot * C::kSlotBytes;
+        if (clean) {
+          const uint32_t bar = smem_u32(&sh.full[slot]);
+          if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlotBytes);
+          __syncwarp();
+          if (lane < (kKeys >> pss)) {
+            const int y = int((int64_t(cur) * a.H_kv + h) << pss);
+#pragma unroll
+            for (int hf = 0; hf < C::kHalves; ++hf)
+              tma_load_2d(dst + hf * (kKeys * 128) + (uint32_t(lane) << (pss + 7)), part ? &tmv : &tmk, hf * 64, y, bar);
+          }
+        } else {
+          const uint8_t* pool = static_cast<const uint8_t*>(part ? a.v : a.k);
+          constexpr int kChunks = D / 8;
+          const int c = ct % kChunks;
+#pragma unroll 8
+          for (int r = ct / kChunks; r < kKeys; r += kCopyThreads / kChunks) {
+            const int64_t off = sh.off[r];
+            cp_async_16(dst + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+                        off >= 0 ? pool + off * (D * 2) + c * 16 : pool, off >= 0 ? 16 : 0);
+          }
+          cp_async_commit();
+          if (kTma) {
+            cp_async_wait<0>();
+            finish(slot);
+          } else {
+            if (pending >= 0) {
+              cp_async_wait<1>();
+              finish(pending);
+            }
+            pending = slot;
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+    if (pending >= 0) finish(pending);
+    if (!ok && steps > 0) {                                        // leave no copy under way (bounded waits)
+      mbar_wait(smem_u32(&sh.q), 0, a.status);
+      for (int x = max(0, seq - C::kSlots); x < seq; ++x)
+        mbar_wait(smem_u32(&sh.full[x % C::kSlots]), (x / C::kSlots) & 1, a.status);
+    }
+  }
+  }
+  if (ns > 1) __threadfence();
+  __syncthreads();
+  if (warp == kMmaWarp) {
+    tc5_fence_after();
+    tc5_dealloc(tmem, 512);
+  }
+  if (ns == 1 || warp >= kMmaWarp) return;
+
+  // ------------------------------------------------------------- merge the parts of the item
+  auto merge_sync = [] { asm volatile("bar.sync 2, %0;\n" ::"n"(kSoftmaxThreads) : "memory"); };
+  if (threadIdx.x == 0) sh.last = atomicAdd(&a.tickets[blockIdx.x], 1) == ns - 1;
+  merge_sync();
+  if (!sh.last) return;
+  __threadfence();
+  float* wgt = reinterpret_cast<float*>(smem);                     // [256][ns], then 1 / sum in [256]
+  float* inv = wgt + 256 * ns;
+  const int64_t part0 = int64_t(blockIdx.x) * ns * 256;
+  auto row_of = [&](int r) -> int64_t {                            // row of q and out, -1: none
+    const int t = (r >> 7) * half_tokens + (r & 127) / G;
+    if ((r & 127) / G >= half_tokens || t >= nt) return -1;
+    return int64_t(c0 + t0 + t) * a.H_q + int64_t(h) * G + (r & 127) % G;
+  };
+  const int mine = threadIdx.x;
+  if (const int64_t orow = row_of(mine); orow >= 0) {
+    const int r = mine;
+    float M = -INFINITY, tot = 0.f;
+    for (int s = 0; s < ns; ++s) {
+      const float x = __ldcg(a.part_lse + part0 + s * 256 + r);
+      wgt[r * ns + s] = x;
+      M = fmaxf(M, x);
+    }
+    for (int s = 0; s < ns; ++s) {
+      const float x = wgt[r * ns + s], w = x == -INFINITY ? 0.f : ex2_approx((x - M) * kLog2e);
+      wgt[r * ns + s] = w;
+      tot += w;
+    }
+    inv[r] = tot > 0.f ? 1.0f / tot : 0.f;
+    if (a.lse) a.lse[orow] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+  }
+  merge_sync();
+  for (int i = threadIdx.x; i < 256 * (D / 4); i += kSoftmaxThreads) {
+    const int r = i / (D / 4), d = 4 * (i % (D / 4));
+    const int64_t orow = row_of(r);
+    if (orow < 0) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int s = 0; s < ns; ++s) {
+      const float w = wgt[r * ns + s];
+      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (part0 + s * 256 + r) * D + d));
+      acc.x = fmaf(w, x.x, acc.x);
+      acc.y = fmaf(w, x.y, acc.y);
+      acc.z = fmaf(w, x.z, acc.z);
+      acc.w = fmaf(w, x.w, acc.w);
+    }
+    const float f = inv[r];
+    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + d) =
+        make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
+  }
+  if (threadIdx.x == 0) a.tickets[blockIdx.x] = 0;
+}
+
+size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+
+// Items of a call: at most one partly filled one per request.
+int64_t items_of(int64_t tokens, int batch, int G) { return tokens / (2 * (128 / G)) + batch; }
+
+// CTAs that share an item's keys: as many as fill the SMs once, where the items
+// alone would leave half of them idle.
+int splits_of(int64_t ctas, int64_t cap_tokens, int sms) {
+  if (2 * ctas > sms) return 1;
+  int64_t s = sms / ctas;
+  const int64_t steps = (cap_tokens + kKeys - 1) / kKeys;
+  if (s > steps) s = steps;
+  if (s > kMaxSplit) s = kMaxSplit;
+  return s < 1 ? 1 : int(s);
+}
+
+struct WsLayout {
+  size_t part_lse, part_o, total;
+};
+// For `ctas` (item, split) pairs. Where a call splits, items x splits <= SMs, so
+// this depends on the call's tokens only through whether it can split at all.
+WsLayout ws_layout(int64_t ctas, int D) {
+  WsLayout w;
+  w.part_lse = align256(size_t(ctas) * 4);
+  w.part_o = w.part_lse + size_t(ctas) * 256 * 4;
+  w.total = w.part_o + size_t(ctas) * 256 * D * 4;
+  return w;
+}
+
+int g_smem[8][64];
+
+template <typename T, int D, bool kTma>
+sa_status launch(const PagedPrefillArgs& a, int splits, cudaStream_t s, const CUtensorMap& mq, const CUtensorMap& mk,
+                 const CUtensorMap& mv, int* cache) {
+  auto k = paged_prefill_kernel<T, D, kTma>;
+  if (!ensure_smem(k, Cfg<D, kTma>::kSmem, cache)) return SA_ERR_CUDA;
+  return launch_ex(k, dim3(unsigned(a.items) * a.H_kv, splits), dim3(kThreads), Cfg<D, kTma>::kSmem, s,
+                   false, 1, a, mq, mk, mv) == cudaSuccess
+             ? SA_OK
+             : SA_ERR_CUDA;
+}
+
 template <typename T, int D>
-sa_status launch(const PagedPrefillArgs& a, unsigned blocks, cudaStream_t s) {
-  paged_prefill_kernel<T, D><<<blocks, kThreads, 0, s>>>(a);
-  return launch_status();
+sa_status dispatch(const PagedPrefillArgs& a, int splits, cudaStream_t s, const sa_cache* c, const void* q, int slot) {
+  CUtensorMap mq = {}, mk = {}, mv = {};
+  if (!make_query_map(&mq, q, D, a.H_q, a.T, a.G, 128 / a.G)) return SA_ERR_CUDA;
+  // a page of 8 rows and more is whole 1024-byte swizzle atoms of a slot
+  if (c->page_size >= 8 && make_pool_map(&mk, c->k, c, c->page_size) && make_pool_map(&mv, c->v, c, c->page_size))
+    return launch<T, D, true>(a, splits, s, mq, mk, mv, g_smem[2 * slot + 1]);
+  return launch<T, D, false>(a, splits, s, mq, mk, mv, g_smem[2 * slot]);
 }
 
 }  // namespace
@@ -200,10 +572,12 @@ sa_status launch(const PagedPrefillArgs& a, unsigned blocks, cudaStream_t s) {
 
 extern "C" size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
                                                   int32_t head_dim, int32_t num_tokens) {
+  using namespace sa;
   if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_tokens < 0 ||
       num_q_heads % num_kv_heads)
     return 0;
-  return 256;
+  const int64_t least = int64_t(batch) * num_kv_heads;             // items of a call of few tokens
+  return 2 * least > sm_count() ? 256 : ws_layout(sm_count(), head_dim).total;
 }
 
 extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
@@ -224,17 +598,27 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
     return SA_ERR_WORKSPACE;
   if (num_tokens == 0) return SA_OK;
   PagedPrefillArgs a = {};
-  a.k = cache->k; a.v = cache->v; a.q = q; a.bt = batch->block_table; a.seq_lens = batch->seq_lens; a.new_cu = new_cu;
+  a.k = cache->k; a.v = cache->v; a.bt = batch->block_table; a.seq_lens = batch->seq_lens; a.new_cu = new_cu;
   a.out = out; a.lse = lse; a.status = dev_status;
   a.H_kv = H; a.H_q = num_q_heads; a.G = G; a.ps_shift = log2i(cache->page_size); a.num_blocks = cache->num_blocks;
   a.bt_stride = batch->bt_stride; a.batch = batch->batch; a.T = num_tokens; a.window = window; a.n_sink = n_sink;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf(float(D))) * kLog2e;
-  // items of kRows / G tokens: at most one partly filled one per request
-  const int per = kRows / G;
-  const int64_t blocks = (num_tokens / per + int64_t(batch->batch)) * H;
-  if (blocks > 0x7fffffff) return SA_ERR_UNSUPPORTED;
+  const int64_t items = items_of(num_tokens, batch->batch, G), ctas = items * H;
+  if (ctas > 0x7fffffff) return SA_ERR_UNSUPPORTED;
+  a.items = int(items);
+  const int64_t seen = window > 0 ? int64_t(window) + n_sink + 3 * kKeys : int64_t(1) << 40;
+  const int64_t cap = int64_t(batch->bt_stride) * cache->page_size;
+  const int splits = splits_of(ctas, cap < seen ? cap : seen, sm_count());
+  if (splits > 1) {
+    const WsLayout w = ws_layout(sm_count(), D);
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    a.tickets = reinterpret_cast<int32_t*>(ws);
+    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+  }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SA_BF16;
-  if (D == 128) return bf ? launch<__nv_bfloat16, 128>(a, unsigned(blocks), s) : launch<__half, 128>(a, unsigned(blocks), s);
-  return bf ? launch<__nv_bfloat16, 64>(a, unsigned(blocks), s) : launch<__half, 64>(a, unsigned(blocks), s);
+  if (D == 128)
+    return bf ? dispatch<__nv_bfloat16, 128>(a, splits, s, cache, q, 0) : dispatch<__half, 128>(a, splits, s, cache, q, 1);
+  return bf ? dispatch<__nv_bfloat16, 64>(a, splits, s, cache, q, 2) : dispatch<__half, 64>(a, splits, s, cache, q, 3);
 }
