@@ -607,7 +607,7 @@ typedef struct sa_rope {
   const void* q_weight;     /* nullable [head_dim], dtype: RMS norm of each query head before the turn */
   const void* k_weight;     /* nullable [head_dim], dtype: the same for keys */
   int32_t max_pos;
-  int32_t rot_dim;          /* columns of a head that are turned, the first ones: 0, 4, 8, .. head_dim */
+  int32_t rot_dim;          /* columns of a head that are turned, the first ones: a multiple of 16, 0 .. head_dim */
   int32_t interleaved;      /* 0: pair i is columns (i, i + rot_dim / 2); otherwise (2i, 2i + 1) */
   int32_t num_axes;         /* 1 .. 4 */
   int32_t sections[4];      /* num_axes > 1: consecutive pairs that turn by each axis, rot_dim / 2 in all */

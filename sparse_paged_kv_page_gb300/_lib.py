@@ -39,7 +39,6 @@ class SaRope(ctypes.Structure):
 
 P_CACHE = ctypes.POINTER(SaCache)
 P_BATCH = ctypes.POINTER(SaBatch)
-P_ROPE = ctypes.POINTER(SaRope)
 c_i64 = ctypes.c_int64
 
 # name -> (restype, argtypes), as declared in include/sparse_attn.h
@@ -87,14 +86,14 @@ SIGNATURES = {
     "sa_shard_selection": (c_i32, [c_ptr, c_ptr, c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_i32, c_ptr,
                                    c_ptr]),
     "sa_merge_states": (c_i32, [c_ptr, c_ptr, c_i32, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr]),
-    "sa_append_kv_rope": (c_i32, [P_CACHE, P_BATCH, P_ROPE, c_ptr, c_i64, c_i32, c_ptr, c_i64, c_ptr,
+    "sa_append_kv_rope": (c_i32, [c_ptr, c_ptr, c_ptr, c_ptr, c_i64, c_i32, c_ptr, c_i64, c_ptr,
                                   c_i64, c_ptr, c_i32, c_i32, c_i32, c_ptr, c_ptr, c_ptr, c_ptr,
                                   c_i32, c_ptr, c_ptr]),
     "sa_paged_decode_workspace_size": (c_size, [c_i32, c_i32, c_i32, c_i32]),
-    "sa_paged_decode": (c_i32, [P_CACHE, P_BATCH, c_ptr, c_i32, c_i32, c_i32, c_f32, c_ptr, c_ptr,
+    "sa_paged_decode": (c_i32, [c_ptr, c_ptr, c_ptr, c_i32, c_i32, c_i32, c_f32, c_ptr, c_ptr,
                                 c_ptr, c_size, c_ptr, c_ptr]),
     "sa_paged_prefill_workspace_size": (c_size, [c_i32, c_i32, c_i32, c_i32, c_i32]),
-    "sa_paged_prefill": (c_i32, [P_CACHE, P_BATCH, c_ptr, c_i32, c_ptr, c_i32, c_i32, c_i32, c_f32,
+    "sa_paged_prefill": (c_i32, [c_ptr, c_ptr, c_ptr, c_i32, c_ptr, c_i32, c_i32, c_i32, c_f32,
                                  c_ptr, c_ptr, c_ptr, c_size, c_ptr, c_ptr]),
     "sa_struct_size": (c_size, [c_i32]),
     "sa_wait_selftest": (c_i32, [c_i32, ctypes.c_int64, c_ptr, c_ptr, c_ptr]),

@@ -442,31 +442,41 @@ def make_rope(table: Optional[torch.Tensor], *, interleaved: bool = False,
     return r
 
 
-def _rows(t, name: str, dtype, heads: Optional[int], head_dim: int):
-    """Address and token stride of rows [T, heads, head_dim] whose tokens may lie apart."""
-    if not t.is_cuda or t.dtype != dtype:
-        raise ValueError(f"{name} must be a CUDA tensor of the cache dtype {dtype}")
-    shape, (stride, head, one) = t.shape, t.stride()
-    if shape[2] != head_dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} must be [T, {heads or 'heads'}, {head_dim}], got {tuple(shape)}")
+def _rows(t, name: str, dtype, heads: int, head_dim: int):
+    """Address and token stride of rows [T, heads, head_dim] whose tokens may lie apart (heads 0: any)."""
+    shape = t.shape
+    if t.dtype != dtype or not t.is_cuda or len(shape) != 3 or shape[2] != head_dim or (heads and shape[1] != heads):
+        raise ValueError(f"{name} must be a CUDA tensor [T, {heads or 'heads'}, {head_dim}] of the cache dtype {dtype}")
+    stride, head, one = t.stride()
     if one != 1 or (head != head_dim and shape[1] > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
     return t.data_ptr(), stride if shape[0] > 1 else max(stride, shape[1] * head_dim)
 
 
-def _launch(fn_name: str, device, stream, args):
+def _whole(t, dtype, name: str):
+    """_p of a tensor that is there, in fewer steps."""
+    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
+        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+    return t.data_ptr()
+
+
+_fns = {}
+
+
+def _launch(fn_name: str, device: int, stream, *args):
     """Call `fn_name(*args, stream)` with `device` current, on its current stream unless one is given."""
-    fn = getattr(_lib.load(), fn_name)
-    dev = device.index
+    fn = _fns.get(fn_name)
+    if fn is None:
+        fn = _fns[fn_name] = getattr(_lib.load(), fn_name)
     if stream is None:
-        s = torch._C._cuda_getCurrentRawStream(dev)
+        stream = torch._C._cuda_getCurrentRawStream(device)
+    elif not isinstance(stream, int):
+        stream = stream.cuda_stream
+    if device == torch._C._cuda_getDevice():
+        st = fn(*args, stream)
     else:
-        s = stream if isinstance(stream, int) else stream.cuda_stream
-    if dev == torch.cuda.current_device():
-        st = fn(*args, s)
-    else:
-        with torch.cuda.device(dev):
-            st = fn(*args, s)
+        with torch.cuda.device(device):
+            st = fn(*args, stream)
     if st != 0:
         raise SaError(fn_name, st)
 
@@ -478,35 +488,41 @@ def sa_append_kv_rope(cache: SaCache, batch: SaBatch, rope: SaRope, q, k_new, v_
     append of k_new and v_new. Tokens may lie apart (slices of one projection's output). advanced: the
     batch's lengths already count the new tokens and stay as they are."""
     pool = cache._keep[0]
-    dt, H, D = pool.dtype, pool.shape[1], pool.shape[3]
+    dt = pool.dtype
+    _, H, _, D = pool.shape
     T = k_new.shape[0]
     kp, ks = _rows(k_new, "k_new", dt, H, D)
     vp, vs = _rows(v_new, "v_new", dt, H, D)
+    if v_new.shape[0] != T:
+        raise ValueError("q, k_new and v_new must have the same tokens")
     qp = qop = None
     qs = hq = 0
     if q is not None:
-        qp, qs = _rows(q, "q", dt, None, D)
-        hq = q.shape[1]
-        if q_out is None or q_out.shape != q.shape or q_out.dtype != dt:
+        qp, qs = _rows(q, "q", dt, 0, D)
+        shape = q.shape
+        hq = shape[1]
+        if shape[0] != T:
+            raise ValueError("q, k_new and v_new must have the same tokens")
+        if q_out is None or q_out.shape != shape:
             raise ValueError("q_out must be like q")
-        qop = _p(q_out, name="q_out")
+        qop = _whole(q_out, dt, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
-    if v_new.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError("q, k_new and v_new must have the same tokens")
     if new_cu.numel() != batch.batch + 1:
         raise ValueError("new_cu must be [batch + 1]")
-    positions, qw, kw = rope._keep[1:]
+    _, positions, qw, kw = rope._keep
     if positions is not None and positions.shape[-1] != T:
         raise ValueError("positions must have one column for each row of k_new")
     for w in (qw, kw):
         if w is not None and (w.dtype != dt or w.numel() != D):
             raise ValueError("q_weight and k_weight must be [head_dim] in the cache dtype")
-    _launch("sa_append_kv_rope", pool.device, stream,
-            (cache, batch, rope, qp, qs, hq, kp, ks, vp, vs, _p(new_cu, torch.int32, "new_cu"), T,
-             max_new_per_req, int(advanced), qop, _p(hh, torch.bfloat16, "hh"),
-             _p(ret_pos, torch.int32, "ret_pos"), _p(ret_cnt, torch.int32, "ret_cnt"), ret_cap,
-             _p(dev_status, torch.int32, "dev_status")))
+    _launch("sa_append_kv_rope", pool.get_device(), stream, ctypes.addressof(cache), ctypes.addressof(batch),
+            ctypes.addressof(rope), qp, qs, hq, kp, ks, vp, vs, _whole(new_cu, torch.int32, "new_cu"), T,
+            max_new_per_req, 1 if advanced else 0, qop,
+            None if hh is None else _whole(hh, torch.bfloat16, "hh"),
+            None if ret_pos is None else _whole(ret_pos, torch.int32, "ret_pos"),
+            None if ret_cnt is None else _whole(ret_cnt, torch.int32, "ret_cnt"), ret_cap,
+            None if dev_status is None else _whole(dev_status, torch.int32, "dev_status"))
 
 
 def sa_paged_decode_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int, head_dim: int) -> int:
@@ -535,17 +551,22 @@ def alloc_paged_prefill_workspace(batch, num_kv_heads, num_q_heads, head_dim, nu
 
 
 def _attention(cache, q, num_q_heads, out, lse, workspace):
-    """Addresses of the rows of an attention call, checked: q, out, lse, workspace and its bytes."""
+    """Addresses of the rows of an attention call, checked: q, out, lse, workspace and its bytes, and the device."""
     pool = cache._keep[0]
-    dt = pool.dtype
-    if q.dim() != 3 or q.shape[1] != num_q_heads or q.shape[2] != pool.shape[3]:
-        raise ValueError(f"q must be [rows, {num_q_heads}, {pool.shape[3]}], got {tuple(q.shape)}")
-    if out.shape != q.shape:
+    dt, shape = pool.dtype, q.shape
+    if len(shape) != 3 or shape[1] != num_q_heads or shape[2] != pool.shape[3]:
+        raise ValueError(f"q must be [rows, {num_q_heads}, {pool.shape[3]}], got {tuple(shape)}")
+    if out.shape != shape:
         raise ValueError("out must be like q")
-    if lse is not None and lse.shape != q.shape[:2]:
-        raise ValueError("lse must be [rows, num_q_heads]")
-    return (_p(q, dt, "q"), _p(out, dt, "out"), _p(lse, torch.float32, "lse"), _p(workspace, name="workspace"),
-            0 if workspace is None else workspace.numel() * workspace.element_size(), pool.device)
+    lp = wp = None
+    wbytes = 0
+    if lse is not None:
+        if lse.shape != shape[:2]:
+            raise ValueError("lse must be [rows, num_q_heads]")
+        lp = _whole(lse, torch.float32, "lse")
+    if workspace is not None:
+        wp, wbytes = _p(workspace, name="workspace"), workspace.nbytes
+    return _whole(q, dt, "q"), _whole(out, dt, "out"), lp, wp, wbytes, pool.get_device()
 
 
 def sa_paged_decode(cache: SaCache, batch: SaBatch, q, num_q_heads: int, scale: float, out, window: int = 0,
@@ -555,9 +576,9 @@ def sa_paged_decode(cache: SaCache, batch: SaBatch, q, num_q_heads: int, scale: 
     qp, op, lp, wp, wbytes, device = _attention(cache, q, num_q_heads, out, lse, workspace)
     if q.shape[0] != batch.batch:
         raise ValueError("q must have one row for each request")
-    _launch("sa_paged_decode", device, stream,
-            (cache, batch, qp, num_q_heads, window, n_sink, scale, op, lp, wp, wbytes,
-             _p(dev_status, torch.int32, "dev_status")))
+    _launch("sa_paged_decode", device, stream, ctypes.addressof(cache), ctypes.addressof(batch), qp, num_q_heads,
+            window, n_sink, scale, op, lp, wp, wbytes,
+            None if dev_status is None else _whole(dev_status, torch.int32, "dev_status"))
 
 
 def sa_paged_prefill(cache: SaCache, batch: SaBatch, q, num_q_heads: int, new_cu, scale: float, out,
@@ -567,6 +588,6 @@ def sa_paged_prefill(cache: SaCache, batch: SaBatch, q, num_q_heads: int, new_cu
     qp, op, lp, wp, wbytes, device = _attention(cache, q, num_q_heads, out, lse, workspace)
     if new_cu.numel() != batch.batch + 1:
         raise ValueError("new_cu must be [batch + 1]")
-    _launch("sa_paged_prefill", device, stream,
-            (cache, batch, qp, num_q_heads, _p(new_cu, torch.int32, "new_cu"), q.shape[0], window, n_sink, scale,
-             op, lp, wp, wbytes, _p(dev_status, torch.int32, "dev_status")))
+    _launch("sa_paged_prefill", device, stream, ctypes.addressof(cache), ctypes.addressof(batch), qp, num_q_heads,
+            _whole(new_cu, torch.int32, "new_cu"), q.shape[0], window, n_sink, scale, op, lp, wp, wbytes,
+            None if dev_status is None else _whole(dev_status, torch.int32, "dev_status"))

@@ -8,13 +8,14 @@
 // (u cos a - v sin a, u sin a + v cos a). All in float32, rounded once to the
 // element type. The statistics are those of sa_append_kv, over the rounded keys.
 //
-// Work split: one warp per (page, KV head) of the new tokens, one warp per
-// (token, chunk of query heads), all in one launch. A row is D / 4 lanes of
-// four columns: lane l holds pairs 2l and 2l + 1, so a rotation needs no other
-// lane, the norm is one butterfly sum, and the page statistics of a column stay
-// in the registers of the lane that owns it. Rows are loaded four at a time.
+// Work split: one warp per (page, group of KV heads) of the new tokens, one warp per
+// (token, chunk of query heads), all in one launch. Lane l of a row
+// holds its pairs N l .. N l + N - 1, N = 8 for queries and 4 for keys (whose statistics
+// take registers), so a rotation needs no other lane and the norm is a butterfly over
+// few of them. The rows that a warp works on at once are heads of one token: they share
+// its angles, and the page statistics of a column stay with the lane that owns it.
 // Every value is read once and written once: HBM bound for prompts, bound by the
-// launch and two dependent loads (lengths, then angles) for single tokens.
+// launch and the dependent loads (lengths, table, page) for single tokens.
 #include "common.cuh"
 #include "host.h"
 #include "page_stats.cuh"
@@ -22,9 +23,20 @@
 namespace sa {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 4;                  // rows a lane has in flight
+constexpr int kKeyPairs = 4, kQueryPairs = 8;   // pairs of columns of a lane
+constexpr int kQueryBatch = 2;                  // rows of queries a lane has in flight beside those at work
+
+// Calls whose warps fit the SMs at once wait for loads: many rows in flight a lane,
+// three blocks an SM. Others need warps: six blocks an SM. Measured (us) as few / many:
+// 16 requests' single tokens with 2048 - 8192 cached 6.1 / 7.7, 4 x 8192 tokens 329 / 247.
+template <bool kFew>
+struct Depth {
+  static constexpr int kBlocks = kFew ? 3 : 6;
+  static constexpr int kOld = kFew ? 8 : 4;     // cached rows
+  static constexpr int kNew = kFew ? 2 : 1;     // tokens of new keys and values beside those at work
+};
 
 struct RopeArgs {
   void* k;
@@ -50,7 +62,8 @@ struct RopeArgs {
   int H, H_q, ps_shift, num_blocks, bt_stride, batch, T, max_new, ret_cap, advanced;
   int max_pos, rot, axes, sec[4];          // sec: first pair of each axis's section
   float eps;
-  int k_units, pages, q_chunk, q_chunks;   // K warps, pages a request can touch, query heads per warp
+  int k_units, pages, k_groups;            // K warps: requests x pages each can touch x groups of KV heads
+  int q_chunk, q_chunks;                   // query heads per warp
 };
 
 // Request with length L and new rows c0 .. c1: old length, tokens kept, first row.
@@ -69,219 +82,315 @@ __device__ __forceinline__ bool plan(const RopeArgs& a, int L, int c0, int c1, b
   return n > 0;
 }
 
+// N words (two elements each, N = 2 or 4) in one access.
+template <int N>
+__device__ __forceinline__ void load_words(uint32_t* w, const void* p) {
+  if constexpr (N == 4) {
+    const uint4 x = *static_cast<const uint4*>(p);
+    w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w;
+  } else {
+    const uint2 x = *static_cast<const uint2*>(p);
+    w[0] = x.x, w[1] = x.y;
+  }
+}
+template <int N>
+__device__ __forceinline__ void store_words(void* p, const uint32_t* w) {
+  if constexpr (N == 4) *static_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *static_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+}
+
+template <int NP>
 struct Turn {
-  float c0, c1, s0, s1;
+  float c[NP], s[NP];
 };
 
-// The columns of one lane: pairs e and e + 1 of the row, as two adjacent column
-// pairs at ca and cb. Half layout: (ca, cb) = (u's, v's); interleaved and beyond
-// the rotated columns: (ca, cb) = (pair e, pair e + 1).
-template <bool kInter>
+// A lane's share of a row: two runs of NP columns, as words of two.
+template <int NP>
+struct Row {
+  uint32_t w[NP];
+};
+
+// The columns of one lane: pairs e .. e + NP - 1 of the row, as NP adjacent columns
+// at ca and NP at cb. Half layout: the u's and the v's of the pairs; interleaved and
+// beyond the rotated columns: 2 NP adjacent columns, pair by pair.
+template <bool kInter, int NP>
 struct Lane {
   int e, ca, cb, ax0, ax1;
   bool turned, split;
   __device__ __forceinline__ Lane(const RopeArgs& a, int l) {
     const int r = a.rot >> 1;
-    e = 2 * l;
+    e = NP * l;
     turned = e < r;
     split = !kInter && turned;
     ca = split ? e : 2 * e;
-    cb = split ? e + r : 2 * e + 2;
-    ax0 = ax1 = 0;
-    for (int x = 1; x < a.axes; ++x) {
-      ax0 += e >= a.sec[x];
-      ax1 += e + 1 >= a.sec[x];
-    }
+    cb = split ? e + r : 2 * e + NP;
+    ax0 = axis(a, e);
+    ax1 = axis(a, e + NP - 1);
   }
-  __device__ __forceinline__ uint2 load(const uint16_t* row) const {
-    if (kInter) return *reinterpret_cast<const uint2*>(row + ca);
-    return make_uint2(*reinterpret_cast<const uint32_t*>(row + ca), *reinterpret_cast<const uint32_t*>(row + cb));
+  static __device__ __forceinline__ int axis(const RopeArgs& a, int e) {
+    int x = 0;
+    for (int i = 1; i < a.axes; ++i) x += e >= a.sec[i];
+    return x;
   }
-  __device__ __forceinline__ void store(uint16_t* row, uint2 w) const {
-    if (kInter) {
-      *reinterpret_cast<uint2*>(row + ca) = w;
-    } else {
-      *reinterpret_cast<uint32_t*>(row + ca) = w.x;
-      *reinterpret_cast<uint32_t*>(row + cb) = w.y;
-    }
+  __device__ __forceinline__ Row<NP> load(const uint16_t* row) const {
+    Row<NP> r;
+    load_words<NP / 2>(r.w, row + ca);
+    load_words<NP / 2>(r.w + NP / 2, row + cb);
+    return r;
   }
-  // Angles of row t of the call (position `pos` where the call gives none).
-  __device__ __forceinline__ Turn angles(const RopeArgs& a, int t, int pos) const {
-    Turn g = {1.f, 1.f, 0.f, 0.f};
-    if (!turned) return g;
-    int p0 = pos, p1 = pos;
-    if (a.positions) {
-      p0 = __ldg(a.positions + int64_t(ax0) * a.T + t);
-      p1 = ax1 == ax0 ? p0 : __ldg(a.positions + int64_t(ax1) * a.T + t);
-    }
-    if (p0 < 0 || p0 >= a.max_pos || p1 < 0 || p1 >= a.max_pos) {
-      flag(a.status, SA_DEV_BAD_POSITION);
-      return g;
-    }
-    const float* f0 = a.table + int64_t(p0) * a.rot + e;
-    if (p0 == p1) {
-      const float2 c = __ldg(reinterpret_cast<const float2*>(f0));
-      const float2 s = __ldg(reinterpret_cast<const float2*>(f0 + (a.rot >> 1)));
-      g = {c.x, c.y, s.x, s.y};
-    } else {
-      const float* f1 = a.table + int64_t(p1) * a.rot + e + 1;
-      g = {__ldg(f0), __ldg(f1), __ldg(f0 + (a.rot >> 1)), __ldg(f1 + (a.rot >> 1))};
-    }
-    return g;
+  __device__ __forceinline__ void store(uint16_t* row, const Row<NP>& r) const {
+    store_words<NP / 2>(row + ca, r.w);
+    store_words<NP / 2>(row + cb, r.w + NP / 2);
   }
-};
-
-// One row: norm over its LPR lanes (weights w of this lane's columns), rotation, rounding.
-template <typename T, int D, bool kInter>
-__device__ __forceinline__ uint2 transform(const Lane<kInter>& ln, uint2 x, const Turn& g, bool norm, const float4& w,
-                                           float eps) {
-  using E = Elem<T>;
-  float a0 = E::lo(x.x), a1 = E::hi(x.x), b0 = E::lo(x.y), b1 = E::hi(x.y);
-  if (norm) {
-    float ss = fmaf(a0, a0, a1 * a1) + fmaf(b0, b0, b1 * b1);
+  // Angles at the positions p of a token on each axis.
+  __device__ __forceinline__ void angles(const RopeArgs& a, const int (&p)[4], Turn<NP>& g) const {
 #pragma unroll
-    for (int o = 1; o < D / 4; o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
-    const float f = rsqrtf(ss * (1.0f / D) + eps);
-    a0 *= f * w.x;
-    a1 *= f * w.y;
-    b0 *= f * w.z;
-    b1 *= f * w.w;
+    for (int i = 0; i < NP; ++i) g.c[i] = 1.f, g.s[i] = 0.f;
+    if (!turned) return;
+    if (ax0 == ax1) {
+      const int pos = pick(p, ax0);
+      if (pos < 0 || pos >= a.max_pos) {
+        flag(a.status, SA_DEV_BAD_POSITION);
+        return;
+      }
+      const float* f = a.table + int64_t(pos) * a.rot + e;
+#pragma unroll
+      for (int i = 0; i < NP; i += 4) {
+        const float4 c = __ldg(reinterpret_cast<const float4*>(f + i));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(f + (a.rot >> 1) + i));
+        g.c[i] = c.x, g.c[i + 1] = c.y, g.c[i + 2] = c.z, g.c[i + 3] = c.w;
+        g.s[i] = s.x, g.s[i + 1] = s.y, g.s[i + 2] = s.z, g.s[i + 3] = s.w;
+      }
+    } else {                                 // a section ends inside the lane's pairs
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const int pos = pick(p, axis(a, e + i));
+        if (pos < 0 || pos >= a.max_pos) {
+          flag(a.status, SA_DEV_BAD_POSITION);
+          continue;
+        }
+        const float* f = a.table + int64_t(pos) * a.rot + e + i;
+        g.c[i] = __ldg(f);
+        g.s[i] = __ldg(f + (a.rot >> 1));
+      }
+    }
   }
-  if (ln.split)
-    return make_uint2(E::pack(a0 * g.c0 - b0 * g.s0, a1 * g.c1 - b1 * g.s1),
-                      E::pack(a0 * g.s0 + b0 * g.c0, a1 * g.s1 + b1 * g.c1));
-  if (ln.turned)
-    return make_uint2(E::pack(a0 * g.c0 - a1 * g.s0, a0 * g.s0 + a1 * g.c0),
-                      E::pack(b0 * g.c1 - b1 * g.s1, b0 * g.s1 + b1 * g.c1));
-  return norm ? make_uint2(E::pack(a0, a1), E::pack(b0, b1)) : x;
-}
-
-template <typename T, bool kInter>
-__device__ __forceinline__ float4 weights(const Lane<kInter>& ln, const void* w) {
-  if (!w) return make_float4(1.f, 1.f, 1.f, 1.f);
-  const uint2 x = ln.load(static_cast<const uint16_t*>(w));
-  return make_float4(Elem<T>::lo(x.x), Elem<T>::hi(x.x), Elem<T>::lo(x.y), Elem<T>::hi(x.y));
-}
-
-// Running statistics of one column.
-struct Column {
-  float mn = INFINITY, mx = -INFINITY, sum = 0.f;
-  bool exact = true;
-  __device__ __forceinline__ void add(float x) {
-    mn = fminf(mn, x);
-    mx = fmaxf(mx, x);
-    two_sum(sum, x, exact);
-  }
-  __device__ __forceinline__ void join(int lanes) {
-    mn = fminf(mn, __shfl_xor_sync(kFull, mn, lanes));
-    mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, lanes));
-    const bool both = __shfl_xor_sync(kFull, exact, lanes) && exact;
-    const float other = __shfl_xor_sync(kFull, sum, lanes);
-    exact = both;
-    two_sum(sum, other, exact);            // an exact sum is the same in either order
+  static __device__ __forceinline__ int pick(const int (&p)[4], int x) {
+    return x == 0 ? p[0] : x == 1 ? p[1] : x == 2 ? p[2] : p[3];
   }
 };
 
-// Statistics of the adjacent columns (2c, 2c + 1) of (block, head), written; rows already in the pool.
-template <typename T>
-__device__ __forceinline__ void write_stats(const RopeArgs& a, const Column& x, const Column& y, int64_t tile, int blk,
-                                            int h, int D, int c, int fill) {
-  using E = Elem<T>;
-  const int C = D / 2;
-  const uint32_t* kp = static_cast<const uint32_t*>(a.k);
-  uint16_t m0 = 0, m1 = 0;
-  const bool ok0 = x.exact && mean_f32<T>(x.sum, fill, m0);
-  const bool ok1 = y.exact && mean_f32<T>(y.sum, fill, m1);
-  if (!ok0 || !ok1) {                      // rare: float64 over the pool's rows
-    double d0 = 0.0, d1 = 0.0;
-    for (int s = 0; s < fill; ++s) {
-      const uint32_t w = kp[(tile + s) * C + c];
-      d0 += double(E::lo(w));
-      d1 += double(E::hi(w));
-    }
-    if (!ok0) m0 = E::from_f64(d0 / double(fill));
-    if (!ok1) m1 = E::from_f64(d1 / double(fill));
-  }
-  uint32_t* m = static_cast<uint32_t*>(a.meta) + (int64_t(blk) * a.H + h) * 3 * C + c;
-  m[0] = E::pack(x.mn, y.mn);
-  m[C] = E::pack(x.mx, y.mx);
-  m[2 * C] = uint32_t(m0) | (uint32_t(m1) << 16);
-  if (a.kstd) page_std_pair<T>(a.kstd, kp, tile, fill, blk, a.H, C, h, c);
+// Positions of row t of the call on each axis, where the call gives them.
+__device__ __forceinline__ void load_positions(const RopeArgs& a, int t, int (&p)[4]) {
+#pragma unroll
+  for (int x = 0; x < 4; ++x) p[x] = a.positions && x < a.axes ? __ldg(a.positions + int64_t(x) * a.T + t) : 0;
 }
 
-// Warp `u`: the new keys and values of one KV head on one page.
-template <typename T, int D, bool kInter>
-__device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
+template <typename T, int NP>
+__device__ __forceinline__ void unpack(float (&x)[2 * NP], const Row<NP>& r) {
+#pragma unroll
+  for (int i = 0; i < NP; ++i) x[2 * i] = Elem<T>::lo(r.w[i]), x[2 * i + 1] = Elem<T>::hi(r.w[i]);
+}
+
+// One row: norm over its lanes (w: the weights of this lane's columns), rotation, rounding.
+template <typename T, int D, bool kInter, int NP>
+__device__ __forceinline__ Row<NP> transform(const Lane<kInter, NP>& ln, const Row<NP>& r, const Turn<NP>& g, bool norm,
+                                             const Row<NP>& w, float eps) {
+  if (!norm && !ln.turned) return r;
+  float x[2 * NP];
+  unpack<T, NP>(x, r);
+  if (norm) {
+    float ss = 0.f, wt[2 * NP];
+    unpack<T, NP>(wt, w);
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+    for (int o = 1; o < D / (2 * NP); o <<= 1) ss += __shfl_xor_sync(kFull, ss, o);
+    const float f = rsqrtf(ss * (1.0f / D) + eps);
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) x[i] *= f * wt[i];
+  }
+  if (ln.split) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float u = x[i], v = x[NP + i];
+      x[i] = u * g.c[i] - v * g.s[i];
+      x[NP + i] = u * g.s[i] + v * g.c[i];
+    }
+  } else if (ln.turned) {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      const float u = x[2 * i], v = x[2 * i + 1];
+      x[2 * i] = u * g.c[i] - v * g.s[i];
+      x[2 * i + 1] = u * g.s[i] + v * g.c[i];
+    }
+  }
+  Row<NP> y;
+#pragma unroll
+  for (int i = 0; i < NP; ++i) y.w[i] = Elem<T>::pack(x[2 * i], x[2 * i + 1]);
+  return y;
+}
+
+template <bool kInter, int NP>
+__device__ __forceinline__ Row<NP> weights(const Lane<kInter, NP>& ln, const void* w) {
+  return w ? ln.load(static_cast<const uint16_t*>(w)) : Row<NP>{};
+}
+
+// Running statistics of a lane's columns.
+template <int NP>
+struct Columns {
+  float mn[2 * NP], mx[2 * NP], sum[2 * NP];
+  uint32_t inexact = 0;                      // bit i: a rounded addition in column i's sum
+  __device__ __forceinline__ Columns() {
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) mn[i] = INFINITY, mx[i] = -INFINITY, sum[i] = 0.f;
+  }
+  template <typename T>
+  __device__ __forceinline__ void add(const Row<NP>& r) {
+    float x[2 * NP];
+    unpack<T, NP>(x, r);
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      mn[i] = fminf(mn[i], x[i]);
+      mx[i] = fmaxf(mx[i], x[i]);
+      bool exact = true;
+      two_sum(sum[i], x[i], exact);
+      inexact |= uint32_t(!exact) << i;
+    }
+  }
+};
+
+// Statistics of the lane's columns of (block, head), written; the page's rows are in the pool.
+template <typename T, int D, int NP>
+__device__ __forceinline__ void write_stats(const RopeArgs& a, const Columns<NP>& st, int64_t tile, int blk, int h,
+                                            int ca, int cb, int fill) {
   using E = Elem<T>;
-  constexpr int LPR = D / 4, RPW = 32 / LPR;
-  const int lane = threadIdx.x & 31, sub = lane / LPR, col = 4 * (lane % LPR);
-  const int h = u % a.H, rest = u / a.H, b = rest / a.pages, i = rest % a.pages;
+  constexpr int C = D / 2;
+  const uint32_t* kp = static_cast<const uint32_t*>(a.k);
+  uint32_t* m = static_cast<uint32_t*>(a.meta) + (int64_t(blk) * a.H + h) * 3 * C;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    uint32_t mn[NP / 2], mx[NP / 2], mean[NP / 2];
+    const int c0 = (half ? cb : ca) >> 1;    // first column pair
+#pragma unroll
+    for (int i = 0; i < NP / 2; ++i) {
+      const int x = NP * half + 2 * i;
+      mn[i] = E::pack(st.mn[x], st.mn[x + 1]);
+      mx[i] = E::pack(st.mx[x], st.mx[x + 1]);
+      uint16_t m0 = 0, m1 = 0;
+      const bool ok0 = !((st.inexact >> x) & 1u) && mean_f32<T>(st.sum[x], fill, m0);
+      const bool ok1 = !((st.inexact >> (x + 1)) & 1u) && mean_f32<T>(st.sum[x + 1], fill, m1);
+      if (!ok0 || !ok1) {                    // rare: float64 over the pool's rows
+        double d0 = 0.0, d1 = 0.0;
+        for (int s = 0; s < fill; ++s) {
+          const uint32_t w = kp[(tile + s) * C + c0 + i];
+          d0 += double(E::lo(w));
+          d1 += double(E::hi(w));
+        }
+        if (!ok0) m0 = E::from_f64(d0 / double(fill));
+        if (!ok1) m1 = E::from_f64(d1 / double(fill));
+      }
+      mean[i] = uint32_t(m0) | (uint32_t(m1) << 16);
+    }
+    store_words<NP / 2>(m + c0, mn);
+    store_words<NP / 2>(m + C + c0, mx);
+    store_words<NP / 2>(m + 2 * C + c0, mean);
+    if (a.kstd)
+      for (int i = 0; i < NP / 2; ++i) page_std_pair<T>(a.kstd, kp, tile, fill, blk, a.H, C, h, c0 + i);
+  }
+}
+
+// Warp `u`: the new keys and values of a group of KV heads on one page.
+template <typename T, int D, bool kInter, bool kFew>
+__device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
+  constexpr int NP = kKeyPairs, LPR = D / (2 * NP), RPW = 32 / LPR, kKeyBatch = Depth<kFew>::kNew, kOldBatch = Depth<kFew>::kOld;
+  const int lane = threadIdx.x & 31, col = 2 * NP * (lane % LPR);
+  const int h = (u % a.k_groups) * RPW + lane / LPR;
+  const int rest = u / a.k_groups, b = rest / a.pages, i = rest % a.pages;
   const int c0 = a.new_cu[b], c1 = a.new_cu[b + 1], L = a.seq_lens[b];
   int L_old, n;
-  if (!plan(a, L, c0, c1, lane == 0 && h == 0 && i == 0, L_old, n)) return;
+  if (!plan(a, L, c0, c1, lane == 0 && u % a.k_groups == 0 && i == 0, L_old, n)) return;
   const int ps = 1 << a.ps_shift;
   const int p = (L_old >> a.ps_shift) + i;
   if (p > ((L_old + n - 1) >> a.ps_shift)) return;
+  const Lane<kInter, NP> ln(a, lane % LPR);
+  const bool on = h < a.H;
+  const int start = p << a.ps_shift;
+  const int s_new = max(0, L_old - start), fill = min(ps, L_old + n - start);
+  const int row0 = c0 + start - L_old;       // row of the call at slot 0
+  const uint16_t* kn = static_cast<const uint16_t*>(a.k_new) + h * D;
+  const uint16_t* vn = static_cast<const uint16_t*>(a.v_new) + h * D + col;
+  Row<NP> x[kKeyBatch], v[kKeyBatch];
+  Turn<NP> g[kKeyBatch];
+  int at[4] = {0, 0, 0, 0};                  // positions of the page's token 32 m + lane, on each axis
+  auto fetch = [&](int s0) {
+#pragma unroll
+    for (int j = 0; j < kKeyBatch; ++j) {
+      const int s = s0 + j, t = row0 + s;
+      if (a.positions && (s == s_new || (s & 31) == 0)) {
+        const int mine = (s & ~31) + lane;
+        if (mine >= s_new && mine < fill) load_positions(a, row0 + mine, at);
+      }
+      int pos[4] = {start + s, 0, 0, 0};
+      if (a.positions) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x)
+          if (x < a.axes) pos[x] = __shfl_sync(kFull, at[x], s & 31);
+      }
+      x[j] = v[j] = Row<NP>{};
+      if (s < fill) {
+        if (on) {
+          x[j] = ln.load(kn + t * a.k_stride);
+          load_words<NP>(v[j].w, vn + t * a.v_stride);
+        }
+        ln.angles(a, pos, g[j]);
+      }
+    }
+  };
   const int blk = a.bt[int64_t(b) * a.bt_stride + p];
+  fetch(s_new);
   if (blk < 0 || blk >= a.num_blocks) {
     if (lane == 0) flag(a.status, SA_DEV_BAD_BLOCK);
     return;
   }
-  const Lane<kInter> ln(a, lane % LPR);
-  const float4 w = weights<T>(ln, a.k_weight);
-  const int start = p << a.ps_shift;
-  const int s_new = max(0, L_old - start), fill = min(ps, L_old + n - start);
+  const Row<NP> w = weights(ln, a.k_weight);
   const int64_t tile = (int64_t(blk) * a.H + h) * ps;
   uint16_t* kp = static_cast<uint16_t*>(a.k) + tile * D;
-  uint16_t* vp = static_cast<uint16_t*>(a.v) + tile * D;
-  const uint16_t* kn = static_cast<const uint16_t*>(a.k_new) + int64_t(h) * D;
-  const uint16_t* vn = static_cast<const uint16_t*>(a.v_new) + int64_t(h) * D + col;
-  Column st[4];
-  for (int s0 = a.meta ? 0 : s_new / RPW * RPW; s0 < fill; s0 += kBatch * RPW) {
-    uint2 x[kBatch], v[kBatch];
-    Turn g[kBatch];
+  uint16_t* vp = static_cast<uint16_t*>(a.v) + tile * D + col;
+  Columns<NP> st;
+  if (a.meta && on) {
+    for (int s0 = 0; s0 < s_new; s0 += kOldBatch) {
+      Row<NP> old[kOldBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int s = s0 + j * RPW + sub, t = c0 + start + s - L_old;
-      x[j] = v[j] = make_uint2(0u, 0u);
-      g[j] = {1.f, 1.f, 0.f, 0.f};
-      if (s >= s_new && s < fill) {
-        x[j] = ln.load(kn + t * a.k_stride);
-        v[j] = __ldg(reinterpret_cast<const uint2*>(vn + t * a.v_stride));
-        g[j] = ln.angles(a, t, start + s);
-      } else if (s < s_new && a.meta) {
-        x[j] = ln.load(kp + s * D);
-      }
+      for (int j = 0; j < kOldBatch; ++j)
+        if (s0 + j < s_new) old[j] = ln.load(kp + (s0 + j) * D);
+#pragma unroll
+      for (int j = 0; j < kOldBatch; ++j)
+        if (s0 + j < s_new) st.template add<T>(old[j]);
     }
+  }
+  __syncwarp();
+  for (int s0 = s_new; s0 < fill; s0 += kKeyBatch) {
+    Row<NP> y[kKeyBatch], z[kKeyBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
-      const int s = s0 + j * RPW + sub;
-      const uint2 y = transform<T, D, kInter>(ln, x[j], g[j], a.k_weight != nullptr, w, a.eps);
-      if (s >= s_new && s < fill) {
-        x[j] = y;
-        ln.store(kp + s * D, y);
-        *reinterpret_cast<uint2*>(vp + s * D + col) = v[j];
-      }
-      if (s < fill) {
-        st[0].add(E::lo(x[j].x));
-        st[1].add(E::hi(x[j].x));
-        st[2].add(E::lo(x[j].y));
-        st[3].add(E::hi(x[j].y));
+    for (int j = 0; j < kKeyBatch; ++j) {
+      y[j] = transform<T, D, kInter, NP>(ln, x[j], g[j], a.k_weight != nullptr, w, a.eps);
+      z[j] = v[j];
+    }
+    if (s0 + kKeyBatch < fill) fetch(s0 + kKeyBatch);
+#pragma unroll
+    for (int j = 0; j < kKeyBatch; ++j) {
+      const int s = s0 + j;
+      if (s < fill && on) {
+        ln.store(kp + s * D, y[j]);
+        store_words<NP>(vp + s * D, z[j].w);
+        if (a.meta) st.template add<T>(y[j]);
       }
     }
   }
-  __syncwarp();                            // the other lanes' rows are in the pool
-  if (a.meta) {
-    if (RPW == 2) {
-#pragma unroll
-      for (int x = 0; x < 4; ++x) st[x].join(LPR);
-    }
-    if (sub == 0) {
-      write_stats<T>(a, st[0], st[1], tile, blk, h, D, ln.ca >> 1, fill);
-      write_stats<T>(a, st[2], st[3], tile, blk, h, D, ln.cb >> 1, fill);
-    }
-  }
-  for (int s = s_new + lane; s < fill; s += 32) {
+  if (!on) return;
+  if (a.meta) write_stats<T, D, NP>(a, st, tile, blk, h, ln.ca, ln.cb, fill);
+  for (int s = s_new + lane % LPR; s < fill; s += LPR) {
     if (a.hh) a.hh[(int64_t(blk) * ps + s) * a.H + h] = 0;
     if (a.ret_pos) {
       const int cpos = a.ret_cnt[b * a.H + h] + (start + s - L_old);
@@ -294,22 +403,24 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
 // Warp `u`: a chunk of the query heads of one token.
 template <typename T, int D, bool kInter>
 __device__ __forceinline__ void query_unit(const RopeArgs& a, int u) {
-  constexpr int LPR = D / 4, RPW = 32 / LPR;
+  constexpr int NP = kQueryPairs, LPR = D / (2 * NP), RPW = 32 / LPR;
   const int lane = threadIdx.x & 31, sub = lane / LPR;
   const int t = u / a.q_chunks, h0 = (u % a.q_chunks) * a.q_chunk, h1 = min(a.H_q, h0 + a.q_chunk);
-  const Lane<kInter> ln(a, lane % LPR);
+  const Lane<kInter, NP> ln(a, lane % LPR);
   const uint16_t* qi = static_cast<const uint16_t*>(a.q_in) + t * a.q_stride;
   uint16_t* qo = static_cast<uint16_t*>(a.q_out) + int64_t(t) * a.H_q * D;
-  uint2 x[kBatch];
+  Row<NP> x[kQueryBatch];
   auto fetch = [&](int h) {
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kQueryBatch; ++j) {
       const int hh = h + j * RPW + sub;
-      x[j] = hh < h1 ? ln.load(qi + hh * D) : make_uint2(0u, 0u);
+      x[j] = hh < h1 ? ln.load(qi + hh * D) : Row<NP>{};
     }
   };
   fetch(h0);
-  const float4 w = weights<T>(ln, a.q_weight);
+  int pos[4];
+  load_positions(a, t, pos);
+  const Row<NP> w = weights(ln, a.q_weight);
   // the token's request: the first whose rows end behind t
   int b = 0, c0 = 0, c1 = 0, L = 0;
   for (int b0 = 0; b0 < a.batch; b0 += 32) {
@@ -324,27 +435,30 @@ __device__ __forceinline__ void query_unit(const RopeArgs& a, int u) {
   }
   int L_old, n;
   if (b >= a.batch || t < c0 || !plan(a, L, c0, c1, false, L_old, n) || t - c0 >= n) return;
-  const Turn g = ln.angles(a, t, L_old + t - c0);
-  for (int h = h0; h < h1; h += kBatch * RPW) {
-    uint2 y[kBatch];
+  Turn<NP> g;
+  if (!a.positions) pos[0] = L_old + t - c0;
+  ln.angles(a, pos, g);
+  __syncwarp();
+  for (int h = h0; h < h1; h += kQueryBatch * RPW) {
+    Row<NP> y[kQueryBatch];
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) y[j] = transform<T, D, kInter>(ln, x[j], g, a.q_weight != nullptr, w, a.eps);
-    if (h + kBatch * RPW < h1) fetch(h + kBatch * RPW);
+    for (int j = 0; j < kQueryBatch; ++j) y[j] = transform<T, D, kInter, NP>(ln, x[j], g, a.q_weight != nullptr, w, a.eps);
+    if (h + kQueryBatch * RPW < h1) fetch(h + kQueryBatch * RPW);
 #pragma unroll
-    for (int j = 0; j < kBatch; ++j) {
+    for (int j = 0; j < kQueryBatch; ++j) {
       const int hh = h + j * RPW + sub;
       if (hh < h1) ln.store(qo + hh * D, y[j]);
     }
   }
 }
 
-template <typename T, int D, bool kInter>
-__global__ void __launch_bounds__(kThreads) rope_append_kernel(const __grid_constant__ RopeArgs a) {
+template <typename T, int D, bool kInter, bool kFew>
+__global__ void __launch_bounds__(kThreads, Depth<kFew>::kBlocks) rope_append_kernel(const __grid_constant__ RopeArgs a) {
   const int k_blocks = (a.k_units + kWarps - 1) / kWarps;
   const int warp = threadIdx.x >> 5;
   if (int(blockIdx.x) < k_blocks) {
     const int u = blockIdx.x * kWarps + warp;
-    if (u < a.k_units) key_unit<T, D, kInter>(a, u);
+    if (u < a.k_units) key_unit<T, D, kInter, kFew>(a, u);
   } else {
     const int u = (blockIdx.x - k_blocks) * kWarps + warp;
     if (u < a.T * a.q_chunks) query_unit<T, D, kInter>(a, u);
@@ -365,7 +479,9 @@ __global__ void rope_advance_kernel(const __grid_constant__ RopeArgs a) {
 
 template <typename T, int D>
 cudaError_t launch(const RopeArgs& a, unsigned blocks, bool inter, cudaStream_t s) {
-  auto k = inter ? rope_append_kernel<T, D, true> : rope_append_kernel<T, D, false>;
+  const bool few = blocks <= unsigned(Depth<true>::kBlocks * sm_count());
+  auto k = few ? (inter ? rope_append_kernel<T, D, true, true> : rope_append_kernel<T, D, false, true>)
+               : (inter ? rope_append_kernel<T, D, true, false> : rope_append_kernel<T, D, false, false>);
   return launch_ex(k, dim3(blocks), dim3(kThreads), 0, s, false, 1, a);
 }
 
@@ -389,7 +505,7 @@ extern "C" sa_status sa_append_kv_rope(const sa_cache* cache, const sa_batch* ba
   if ((ret_pos == nullptr) != (ret_cnt == nullptr) || (ret_pos && ret_cap <= 0)) return SA_ERR_INVALID_ARG;
   if (cache->kstd && !cache->meta) return SA_ERR_INVALID_ARG;
   const int D = cache->head_dim, H = cache->num_kv_heads;
-  if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 4) return SA_ERR_INVALID_ARG;
+  if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 16) return SA_ERR_INVALID_ARG;
   if (rope->rot_dim && (!rope->table || rope->max_pos <= 0)) return SA_ERR_INVALID_ARG;
   if (rope->num_axes < 1 || rope->num_axes > 4 || (rope->num_axes > 1 && !rope->positions)) return SA_ERR_INVALID_ARG;
   if (!(rope->eps >= 0.f)) return SA_ERR_INVALID_ARG;
@@ -422,9 +538,11 @@ extern "C" sa_status sa_append_kv_rope(const sa_cache* cache, const sa_batch* ba
   a.max_pos = rope->max_pos; a.rot = rope->rot_dim; a.axes = rope->num_axes; a.eps = rope->eps;
   // n tokens from any slot touch at most (n + ps - 2) / ps + 1 pages
   a.pages = int((int64_t(a.max_new) + cache->page_size - 2) / cache->page_size) + 1;
-  const int64_t k_units = int64_t(batch->batch) * a.pages * H;
-  // query heads per warp: few where tokens are few, up to 32 where one read of the angles serves more heads
-  a.q_chunk = 4;
+  const int k_rows = 64 * kKeyPairs / D, rows = 64 * kQueryPairs / D;   // heads a warp works on at once
+  a.k_groups = (H + k_rows - 1) / k_rows;
+  const int64_t k_units = int64_t(batch->batch) * a.pages * a.k_groups;
+  // query heads per warp: one batch where tokens are few, more where one read of the angles can serve them
+  a.q_chunk = rows;
   const int64_t full = int64_t(sm_count()) * 64;
   while (q && a.q_chunk < 32 && a.q_chunk < num_q_heads && int64_t(num_tokens) * num_q_heads / (2 * a.q_chunk) >= full)
     a.q_chunk *= 2;

@@ -66,7 +66,7 @@ def _append(lens, new, *, rot=None, interleaved=False, sections=None, norm=True,
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "fp16"])
-@pytest.mark.parametrize("D,rot", [(128, 128), (64, 64), (128, 64), (64, 20), (128, 0)])
+@pytest.mark.parametrize("D,rot", [(128, 128), (64, 64), (128, 64), (64, 16), (128, 96), (128, 0)])
 @pytest.mark.parametrize("interleaved", [False, True])
 def test_append_rotation_forms(dtype, D, rot, interleaved):
     _append([5, 0, 31], [18, 7, 1], dtype=dtype, D=D, rot=rot, interleaved=interleaved, norm=rot != 64, pad=3)

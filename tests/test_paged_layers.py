@@ -37,7 +37,7 @@ def _append(lib, q=P(0x500000), qs=512, hq=4, k=P(0x600000), ks=256, v=P(0x70000
 @pytest.mark.parametrize("change", [
     dict(k=None), dict(v=None), dict(cu=None), dict(out=None), dict(q=None), dict(hq=0), dict(T=-1), dict(most=-1),
     dict(qs=508), dict(ks=128), dict(vs=260), dict(q=P(0x500008)), dict(out=P(0x900004)), dict(table=P(0x400008)),
-    dict(table=None), dict(max_pos=0), dict(rot_dim=130), dict(rot_dim=132), dict(rot_dim=-4), dict(rot_dim=6),
+    dict(table=None), dict(max_pos=0), dict(rot_dim=130), dict(rot_dim=132), dict(rot_dim=-4), dict(rot_dim=20),
     dict(num_axes=0), dict(num_axes=5), dict(num_axes=2), dict(pos=P(0x1000)), dict(pos=P(0x1000), cnt=P(0x2000)),
     dict(eps=-1.0), dict(eps=float("nan")), dict(dtype=2), dict(batch=0), dict(q_weight=P(0x1004)),
     dict(meta=None, kstd=P(0x1000))])
