@@ -30,7 +30,8 @@ constexpr int kQueryBatch = 2;                  // rows of queries a lane has in
 
 // Calls whose warps fit the SMs at once wait for loads: many rows in flight a lane,
 // three blocks an SM. Others need warps: six blocks an SM. Measured (us) as few / many:
-// 16 requests' single tokens with 2048 - 8192 cached 6.1 / 7.7, 4 x 8192 tokens 329 / 247.
+// 16 requests' single tokens with 2048 - 8192 cached 6.0 / 7.7, 4 x 8192 tokens 329 / 238
+// (1.37 GB: 85% of the measured copy bandwidth).
 template <bool kFew>
 struct Depth {
   static constexpr int kBlocks = kFew ? 3 : 6;
@@ -115,7 +116,8 @@ struct Row {
 // beyond the rotated columns: 2 NP adjacent columns, pair by pair.
 template <bool kInter, int NP>
 struct Lane {
-  int e, ca, cb, ax0, ax1;
+  int e, ca, cb;
+  int first[NP / 4], last[NP / 4];           // axes of the ends of each four pairs
   bool turned, split;
   __device__ __forceinline__ Lane(const RopeArgs& a, int l) {
     const int r = a.rot >> 1;
@@ -124,8 +126,11 @@ struct Lane {
     split = !kInter && turned;
     ca = split ? e : 2 * e;
     cb = split ? e + r : 2 * e + NP;
-    ax0 = axis(a, e);
-    ax1 = axis(a, e + NP - 1);
+#pragma unroll
+    for (int i = 0; i < NP / 4; ++i) {
+      first[i] = axis(a, e + 4 * i);
+      last[i] = axis(a, e + 4 * i + 3);
+    }
   }
   static __device__ __forceinline__ int axis(const RopeArgs& a, int e) {
     int x = 0;
@@ -142,36 +147,36 @@ struct Lane {
     store_words<NP / 2>(row + ca, r.w);
     store_words<NP / 2>(row + cb, r.w + NP / 2);
   }
-  // Angles at the positions p of a token on each axis.
+  // Angles at the positions p of a token on each axis, four pairs at a time where they share one.
   __device__ __forceinline__ void angles(const RopeArgs& a, const int (&p)[4], Turn<NP>& g) const {
 #pragma unroll
     for (int i = 0; i < NP; ++i) g.c[i] = 1.f, g.s[i] = 0.f;
     if (!turned) return;
-    if (ax0 == ax1) {
-      const int pos = pick(p, ax0);
-      if (pos < 0 || pos >= a.max_pos) {
-        flag(a.status, SA_DEV_BAD_POSITION);
-        return;
-      }
-      const float* f = a.table + int64_t(pos) * a.rot + e;
 #pragma unroll
-      for (int i = 0; i < NP; i += 4) {
-        const float4 c = __ldg(reinterpret_cast<const float4*>(f + i));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(f + (a.rot >> 1) + i));
-        g.c[i] = c.x, g.c[i + 1] = c.y, g.c[i + 2] = c.z, g.c[i + 3] = c.w;
-        g.s[i] = s.x, g.s[i + 1] = s.y, g.s[i + 2] = s.z, g.s[i + 3] = s.w;
-      }
-    } else {                                 // a section ends inside the lane's pairs
-#pragma unroll
-      for (int i = 0; i < NP; ++i) {
-        const int pos = pick(p, axis(a, e + i));
+    for (int i = 0; i < NP; i += 4) {
+      if (first[i / 4] == last[i / 4]) {
+        const int pos = pick(p, first[i / 4]);
         if (pos < 0 || pos >= a.max_pos) {
           flag(a.status, SA_DEV_BAD_POSITION);
           continue;
         }
         const float* f = a.table + int64_t(pos) * a.rot + e + i;
-        g.c[i] = __ldg(f);
-        g.s[i] = __ldg(f + (a.rot >> 1));
+        const float4 c = __ldg(reinterpret_cast<const float4*>(f));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(f + (a.rot >> 1)));
+        g.c[i] = c.x, g.c[i + 1] = c.y, g.c[i + 2] = c.z, g.c[i + 3] = c.w;
+        g.s[i] = s.x, g.s[i + 1] = s.y, g.s[i + 2] = s.z, g.s[i + 3] = s.w;
+      } else {                               // a section ends inside them
+#pragma unroll
+        for (int x = i; x < i + 4; ++x) {
+          const int pos = pick(p, axis(a, e + x));
+          if (pos < 0 || pos >= a.max_pos) {
+            flag(a.status, SA_DEV_BAD_POSITION);
+            continue;
+          }
+          const float* f = a.table + int64_t(pos) * a.rot + e + x;
+          g.c[x] = __ldg(f);
+          g.s[x] = __ldg(f + (a.rot >> 1));
+        }
       }
     }
   }
@@ -236,23 +241,45 @@ __device__ __forceinline__ Row<NP> weights(const Lane<kInter, NP>& ln, const voi
   return w ? ln.load(static_cast<const uint16_t*>(w)) : Row<NP>{};
 }
 
-// Running statistics of a lane's columns.
-template <int NP>
+// Packed minimum and maximum of two elements; a NaN loses to a number.
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmin2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, __nv_bfloat16) {
+  const __nv_bfloat162 r = __hmax2(*reinterpret_cast<__nv_bfloat162*>(&x), *reinterpret_cast<__nv_bfloat162*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t min2(uint32_t x, uint32_t y, __half) {
+  const __half2 r = __hmin2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, __half) {
+  const __half2 r = __hmax2(*reinterpret_cast<__half2*>(&x), *reinterpret_cast<__half2*>(&y));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// Running statistics of a lane's columns; minimum and maximum in the elements' own type.
+template <typename T, int NP>
 struct Columns {
-  float mn[2 * NP], mx[2 * NP], sum[2 * NP];
+  uint32_t mn[NP], mx[NP];
+  float sum[2 * NP];
   uint32_t inexact = 0;                      // bit i: a rounded addition in column i's sum
   __device__ __forceinline__ Columns() {
+    const uint32_t inf = Elem<T>::pack(INFINITY, INFINITY);
 #pragma unroll
-    for (int i = 0; i < 2 * NP; ++i) mn[i] = INFINITY, mx[i] = -INFINITY, sum[i] = 0.f;
+    for (int i = 0; i < NP; ++i) mn[i] = inf, mx[i] = inf | 0x80008000u, sum[2 * i] = sum[2 * i + 1] = 0.f;
   }
-  template <typename T>
   __device__ __forceinline__ void add(const Row<NP>& r) {
     float x[2 * NP];
     unpack<T, NP>(x, r);
 #pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      mn[i] = min2(mn[i], r.w[i], T());
+      mx[i] = max2(mx[i], r.w[i], T());
+    }
+#pragma unroll
     for (int i = 0; i < 2 * NP; ++i) {
-      mn[i] = fminf(mn[i], x[i]);
-      mx[i] = fmaxf(mx[i], x[i]);
       bool exact = true;
       two_sum(sum[i], x[i], exact);
       inexact |= uint32_t(!exact) << i;
@@ -260,43 +287,43 @@ struct Columns {
   }
 };
 
+// Rare: the float64 mean of a column (half `hi` of words p, p + C, ..) of the pool.
+template <typename T>
+__device__ __noinline__ uint16_t mean_f64(const uint32_t* p, int C, int fill, bool hi) {
+  double d = 0.0;
+  for (int s = 0; s < fill; ++s) {
+    const uint32_t w = p[int64_t(s) * C];
+    d += double(hi ? Elem<T>::hi(w) : Elem<T>::lo(w));
+  }
+  return Elem<T>::from_f64(d / double(fill));
+}
+
 // Statistics of the lane's columns of (block, head), written; the page's rows are in the pool.
 template <typename T, int D, int NP>
-__device__ __forceinline__ void write_stats(const RopeArgs& a, const Columns<NP>& st, int64_t tile, int blk, int h,
+__device__ __forceinline__ void write_stats(const RopeArgs& a, const Columns<T, NP>& st, int64_t tile, int blk, int h,
                                             int ca, int cb, int fill) {
-  using E = Elem<T>;
   constexpr int C = D / 2;
-  const uint32_t* kp = static_cast<const uint32_t*>(a.k);
+  const uint32_t* kp = static_cast<const uint32_t*>(a.k) + tile * C;
   uint32_t* m = static_cast<uint32_t*>(a.meta) + (int64_t(blk) * a.H + h) * 3 * C;
 #pragma unroll
   for (int half = 0; half < 2; ++half) {
-    uint32_t mn[NP / 2], mx[NP / 2], mean[NP / 2];
+    uint32_t mean[NP / 2];
     const int c0 = (half ? cb : ca) >> 1;    // first column pair
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) {
       const int x = NP * half + 2 * i;
-      mn[i] = E::pack(st.mn[x], st.mn[x + 1]);
-      mx[i] = E::pack(st.mx[x], st.mx[x + 1]);
       uint16_t m0 = 0, m1 = 0;
-      const bool ok0 = !((st.inexact >> x) & 1u) && mean_f32<T>(st.sum[x], fill, m0);
-      const bool ok1 = !((st.inexact >> (x + 1)) & 1u) && mean_f32<T>(st.sum[x + 1], fill, m1);
-      if (!ok0 || !ok1) {                    // rare: float64 over the pool's rows
-        double d0 = 0.0, d1 = 0.0;
-        for (int s = 0; s < fill; ++s) {
-          const uint32_t w = kp[(tile + s) * C + c0 + i];
-          d0 += double(E::lo(w));
-          d1 += double(E::hi(w));
-        }
-        if (!ok0) m0 = E::from_f64(d0 / double(fill));
-        if (!ok1) m1 = E::from_f64(d1 / double(fill));
-      }
+      if (((st.inexact >> x) & 1u) || !mean_f32<T>(st.sum[x], fill, m0)) m0 = mean_f64<T>(kp + c0 + i, C, fill, false);
+      if (((st.inexact >> (x + 1)) & 1u) || !mean_f32<T>(st.sum[x + 1], fill, m1))
+        m1 = mean_f64<T>(kp + c0 + i, C, fill, true);
       mean[i] = uint32_t(m0) | (uint32_t(m1) << 16);
     }
-    store_words<NP / 2>(m + c0, mn);
-    store_words<NP / 2>(m + C + c0, mx);
+    store_words<NP / 2>(m + c0, st.mn + NP / 2 * half);
+    store_words<NP / 2>(m + C + c0, st.mx + NP / 2 * half);
     store_words<NP / 2>(m + 2 * C + c0, mean);
     if (a.kstd)
-      for (int i = 0; i < NP / 2; ++i) page_std_pair<T>(a.kstd, kp, tile, fill, blk, a.H, C, h, c0 + i);
+      for (int i = 0; i < NP / 2; ++i)
+        page_std_pair<T>(a.kstd, static_cast<const uint32_t*>(a.k), tile, fill, blk, a.H, C, h, c0 + i);
   }
 }
 
@@ -357,7 +384,7 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
   const int64_t tile = (int64_t(blk) * a.H + h) * ps;
   uint16_t* kp = static_cast<uint16_t*>(a.k) + tile * D;
   uint16_t* vp = static_cast<uint16_t*>(a.v) + tile * D + col;
-  Columns<NP> st;
+  Columns<T, NP> st;
   if (a.meta && on) {
     for (int s0 = 0; s0 < s_new; s0 += kOldBatch) {
       Row<NP> old[kOldBatch];
@@ -366,7 +393,7 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
         if (s0 + j < s_new) old[j] = ln.load(kp + (s0 + j) * D);
 #pragma unroll
       for (int j = 0; j < kOldBatch; ++j)
-        if (s0 + j < s_new) st.template add<T>(old[j]);
+        if (s0 + j < s_new) st.add(old[j]);
     }
   }
   __syncwarp();
@@ -384,7 +411,7 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
       if (s < fill && on) {
         ln.store(kp + s * D, y[j]);
         store_words<NP>(vp + s * D, z[j].w);
-        if (a.meta) st.template add<T>(y[j]);
+        if (a.meta) st.add(y[j]);
       }
     }
   }
