@@ -28,6 +28,15 @@ struct Span {
   __device__ __forceinline__ int start(int t) const { return (t < sink_tiles ? t : t - sink_tiles + win_tile) * R; }
 };
 
+// One more part of a unit is in memory: parts counted before it. Called by one
+// thread after the block's barrier; publishes the block's writes, and makes the
+// other parts' visible to the block after its next barrier.
+__device__ __forceinline__ int ticket(int32_t* counter) {
+  int old;
+  asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;\n" : "=r"(old) : "l"(counter) : "memory");
+  return old;
+}
+
 // 16 rows x D columns of 2-byte elements in shared memory: 64-column halves of
 // 16 x 128 bytes, 16-byte chunk c of row r at chunk c ^ (r & 7), the TMA engine's
 // 128-byte swizzle.

@@ -69,8 +69,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   using E = Elem<T>;
   using TL = Tile<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ int s_pre[kMaxBatch + 1];         // groups before each request
-  __shared__ int s_scan[32];
   __shared__ uint32_t s_mask[kWarps][kStages];
   __shared__ __align__(8) uint64_t s_bar[kWarps][kStages];
   __shared__ int s_last;
@@ -89,33 +87,21 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&s_bar[w][s]), 1);
     mbar_init_fence();
   }
-  // groups of every request (an empty one has a group too: its outputs are written)
-  {
-    constexpr int kPer = kMaxBatch / kThreads;
-    int n[kPer], sum = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int b = threadIdx.x * kPer + i;
-      n[i] = 0;
-      if (b < a.batch) {
-        const int L = a.seq_lens[b];
-        if (blockIdx.x == 0 && L < 0) flag(a.status, SA_DEV_BAD_COUNT);
-        if (blockIdx.x == 0 && L > cap) flag(a.status, SA_DEV_OVERFLOW);
-        n[i] = a.H_kv * max(1, (span(max(0, L)).tiles + 3) >> 2);
-      }
-      sum += n[i];
+  // Groups of a request (an empty one has a group per head too: its outputs are written). Every warp finds its
+  // places by itself, 32 requests at a time.
+  auto groups_of = [&](int b0) {
+    if (b0 + lane >= a.batch) return 0;
+    const int L = a.seq_lens[b0 + lane];
+    if (blockIdx.x == 0 && threadIdx.x < 32) {
+      if (L < 0) flag(a.status, SA_DEV_BAD_COUNT);
+      if (L > cap) flag(a.status, SA_DEV_OVERFLOW);
     }
-    int total, pre = block_exclusive_scan<kThreads>(sum, s_scan, &total);
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-      const int b = threadIdx.x * kPer + i;
-      if (b <= a.batch) s_pre[b] = pre;
-      pre += n[i];
-    }
-    if (threadIdx.x == 0) s_pre[a.batch] = total;
-    __syncthreads();
-  }
-  const int64_t total = s_pre[a.batch], N = min(int64_t(gridDim.x), total);   // every CTA has a group
+    return a.H_kv * max(1, (span(max(0, L)).tiles + 3) >> 2);
+  };
+  const int head_groups = groups_of(0);          // of requests 0 .. 31
+  int all = head_groups;
+  for (int b0 = 32; b0 < a.batch; b0 += 32) all += groups_of(b0);
+  const int64_t total = __reduce_add_sync(kFull, all), N = min(int64_t(gridDim.x), total);   // every CTA has a group
   if (blockIdx.x >= N) return;
   int at = int(total * blockIdx.x / N);
   const int stop = int(total * (int64_t(blockIdx.x) + 1) / N);
@@ -125,11 +111,27 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   bool alive = true;
 
   while (at < stop) {
-    int b = 0;
-    for (int step = kMaxBatch; step; step >>= 1)
-      if (b + step < a.batch && s_pre[b + step] <= at) b += step;
-    const int groups = (s_pre[b + 1] - s_pre[b]) / a.H_kv;
-    const int h = (at - s_pre[b]) / groups, unit_at = s_pre[b] + h * groups;
+    // the request and head of group `at`
+    int b = 0, before = 0, mine = 0;
+    for (int b0 = 0; b0 < a.batch; b0 += 32) {
+      const int x = b0 ? groups_of(b0) : head_groups;
+      int sum = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const int k = __popc(__ballot_sync(kFull, before + sum <= at));
+      if (k < 32) {
+        b = b0 + k;
+        mine = __shfl_sync(kFull, x, k);
+        before += __shfl_sync(kFull, sum, k) - mine;
+        break;
+      }
+      before += __shfl_sync(kFull, sum, 31);
+    }
+    const int groups = mine / a.H_kv;
+    const int h = (at - before) / groups, unit_at = before + h * groups;
     const int gi = at - unit_at, ge = min(groups, gi + stop - at);
     at += ge - gi;
     const int L = length(b), Lc = min(L, cap);
@@ -399,45 +401,49 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int c_first = int(((int64_t(unit_at) + 1) * N - 1) / total);
       const int c_last = int(((int64_t(unit_at) + groups) * N - 1) / total);
       const int parts = c_last - c_first + 1;
-      __threadfence();
       __syncthreads();
       const int unit = b * a.H_kv + h;
-      if (threadIdx.x == 0) s_last = atomicAdd(&a.tickets[unit], 1) == parts - 1;
+      if (threadIdx.x == 0) s_last = ticket(&a.tickets[unit]) == parts - 1;
       __syncthreads();
       if (s_last) {
-        __threadfence();
-        float* wgt = reinterpret_cast<float*>(smem);      // [parts][G]
+        // a thread merges four columns of a row, eight parts in flight, in the order of the parts
         auto slot_of = [&](int p) { return 2 * int64_t(c_first + p) + (p == 0 ? 1 : 0); };
-        for (int i = threadIdx.x; i < parts * G; i += kThreads) wgt[i] = __ldcg(a.part_lse + slot_of(i / G) * G + i % G);
-        __syncthreads();
-        if (threadIdx.x < G) {
-          const int row = threadIdx.x;
-          float M = -INFINITY, tot = 0.f;
-          for (int p = 0; p < parts; ++p) M = fmaxf(M, wgt[p * G + row]);
-          for (int p = 0; p < parts; ++p) {
-            const float v = wgt[p * G + row];
-            const float w = v == -INFINITY ? 0.f : ex2_approx((v - M) * kLog2e);
-            wgt[p * G + row] = w;
-            tot += w;
-          }
-          s_sf[0][row] = tot > 0.f ? 1.0f / tot : 0.f;
-          if (a.lse) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
-        }
-        __syncthreads();
         for (int idx = 4 * threadIdx.x; idx < G * D; idx += 4 * kThreads) {
           const int row = idx / D;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-          for (int p = 0; p < parts; ++p) {
-            const float w = wgt[p * G + row];
-            const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + slot_of(p) * G * D + idx));
-            acc.x = fmaf(w, x.x, acc.x);
-            acc.y = fmaf(w, x.y, acc.y);
-            acc.z = fmaf(w, x.z, acc.z);
-            acc.w = fmaf(w, x.w, acc.w);
+          float M = -INFINITY, tot = 0.f;
+          for (int p0 = 0; p0 < parts; p0 += 8) {
+            float4 x[8];
+            float z[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              z[k] = -INFINITY;
+              if (p0 + k < parts) {
+                const int64_t r = slot_of(p0 + k) * G;
+                z[k] = __ldcg(a.part_lse + r + row);
+                x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + r * D + idx));
+              }
+            }
+            float m = M;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) m = fmaxf(m, z[k]);
+            const float f = M == -INFINITY ? 0.f : ex2_approx((M - m) * kLog2e);
+            tot *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+            M = m;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              if (z[k] == -INFINITY) continue;             // an empty part
+              const float w = ex2_approx((z[k] - M) * kLog2e);
+              tot += w;
+              acc.x = fmaf(w, x[k].x, acc.x);
+              acc.y = fmaf(w, x[k].y, acc.y);
+              acc.z = fmaf(w, x[k].z, acc.z);
+              acc.w = fmaf(w, x[k].w, acc.w);
+            }
           }
-          const float f = s_sf[0][row];
+          const float f = tot > 0.f ? 1.0f / tot : 0.f;
           *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
+          if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
         }
         if (threadIdx.x == 0) a.tickets[unit] = 0;
       }

@@ -454,7 +454,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
   }
   }
-  if (ns > 1) __threadfence();
   __syncthreads();
   if (warp == kMmaWarp) {
     tc5_fence_after();
@@ -464,10 +463,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   // ------------------------------------------------------------- merge the parts of the item
   auto merge_sync = [] { asm volatile("bar.sync 2, %0;\n" ::"n"(kSoftmaxThreads) : "memory"); };
-  if (threadIdx.x == 0) sh.last = atomicAdd(&a.tickets[blockIdx.x], 1) == ns - 1;
+  if (threadIdx.x == 0) sh.last = ticket(&a.tickets[blockIdx.x]) == ns - 1;
   merge_sync();
   if (!sh.last) return;
-  __threadfence();
   float* wgt = reinterpret_cast<float*>(smem);                     // [256][ns], then 1 / sum in [256]
   float* inv = wgt + 256 * ns;
   const int64_t part0 = int64_t(blockIdx.x) * ns * 256;
