@@ -52,7 +52,6 @@ struct PagedDecodeArgs {
 template <int D>
 struct Tile {
   static constexpr int kBytes = 16 * D * 2;
-  static constexpr int kHalves = D / 64;
   static constexpr int kChunks = D / 8;
   static constexpr int kRowsPerOp = 32 / kChunks;
   static constexpr int kOps = 16 / kRowsPerOp;
@@ -198,11 +197,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
           mbar_arrive_expect_tx(bar, vmask ? uint32_t(TL::kStageBytes) : 0u);
           if (vmask) {
             const int y = int(((int64_t(blk) * a.H_kv + h) << pss) + (j0 & ((1 << pss) - 1)));
-#pragma unroll
-            for (int hf = 0; hf < TL::kHalves; ++hf) {
-              tma_load_2d(sk + hf * 2048, &tmk, hf * 64, y, bar);
-              tma_load_2d(sv + hf * 2048, &tmv, hf * 64, y, bar);
-            }
+            tma_load_3d(sk, &tmk, 0, y, 0, bar);
+            tma_load_3d(sv, &tmv, 0, y, 0, bar);
           }
         }
       } else {
@@ -480,7 +476,7 @@ sa_status launch(const PagedDecodeArgs& a, int ctas, cudaStream_t s, const CUten
 template <typename T, int D>
 sa_status dispatch(const PagedDecodeArgs& a, int ctas, cudaStream_t s, const sa_cache* c, int slot) {
   CUtensorMap mk = {}, mv = {};
-  if (c->page_size >= 16 && make_pool_map(&mk, c->k, c, 16) && make_pool_map(&mv, c->v, c, 16))
+  if (c->page_size >= 16 && make_row_map(&mk, c->k, c) && make_row_map(&mv, c->v, c))
     return launch<T, D, true>(a, ctas, s, mk, mv, g_smem[2 * slot + 1]);
   return launch<T, D, false>(a, ctas, s, mk, mv, g_smem[2 * slot]);
 }

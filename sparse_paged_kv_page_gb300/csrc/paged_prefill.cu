@@ -63,7 +63,8 @@ template <int D, bool kTma>
 struct Cfg {
   static constexpr int kProducers = kTma ? 1 : 3;                  // copy warps
   static constexpr int kHalves = D / 64;                           // 64-column halves of a row
-  static constexpr int kSlotBytes = kHalves * kKeys * 128;
+  static constexpr int kGroupBytes = kHalves * 1024;               // 8 rows of a slot: [half][8 rows of 128 bytes]
+  static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kQBytes = 2 * kSlotBytes;
   static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + 1024;
@@ -77,10 +78,13 @@ struct Shared {
   int abort, last;
 };
 
-// Wait for a phase; false once any wait of the CTA has given up.
+// Wait for a phase; false once any wait of the CTA has given up. The clock is read
+// only after many tries (each try suspends the thread for a while by itself).
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared& sh, int32_t* status) {
   const uint32_t b = smem_u32(bar);
-  if (mbar_try_wait(b, parity)) return true;
+#pragma unroll 1
+  for (int i = 0; i < 256; ++i)
+    if (mbar_try_wait(b, parity)) return true;
   const uint64_t t0 = global_ns();
   while (true) {
 #pragma unroll 1
@@ -274,22 +278,28 @@ __global__ void __launch_bounds__(kThreads, 1)
   asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
   if (warp == kMmaWarp) {
     // ------------------------------------------------------------- products, issued by one thread
-    if (lane == 0 && steps > 0) {
+    if (steps > 0 && elect_one()) {
       constexpr uint32_t id_s = tc5_idesc(kBf16, 128, kKeys, false), id_o = tc5_idesc(kBf16, 128, D, true);
-      const uint32_t q_addr = smem_u32(smem), r_addr = smem_u32(ring);
+      const uint64_t q_desc = tc5_desc(smem_u32(smem), 16, 1024);
+      const uint64_t k_desc = tc5_desc(smem_u32(ring), 16, C::kGroupBytes);
+      const uint64_t v_desc = tc5_desc(smem_u32(ring), 1024, C::kGroupBytes);
       auto scores = [&](int tile, int slot) {                       // S = Q K^T
+        const uint64_t qd = q_desc + uint32_t(tile * C::kSlotBytes / 16), kd = k_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
-          const uint32_t in_row = (kk >> 2) * (kKeys * 128) + (kk & 3) * 32;
-          tc5_mma_ss(tmem + tile * 128, tc5_desc(q_addr + tile * C::kSlotBytes + in_row, 16, 1024),
-                     tc5_desc(r_addr + slot * C::kSlotBytes + in_row, 16, 1024), id_s, kk > 0);
+          const uint32_t q_at = (kk >> 2) * (128 * 128) + (kk & 3) * 32, k_at = (kk >> 2) * 1024 + (kk & 3) * 32;
+          tc5_mma_ss(tmem + tile * 128, qd + q_at / 16, kd + k_at / 16, id_s, kk > 0);
         }
       };
-      auto outputs = [&](int tile, int slot, bool add) {            // O += P V
+      auto outputs = [&](int tile, int slot, bool add, uint32_t parity) {   // O += P V once P is there
+        if (!wait_on(&sh.p[tile], parity, sh, a.status)) return false;
+        tc5_fence_after();
+        const uint64_t vd = v_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc5_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + kk * 8,
-                     tc5_desc(r_addr + slot * C::kSlotBytes + kk * 2048, kKeys * 128, 1024), id_o, add || kk > 0);
+          tc5_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
+                     add || kk > 0);
+        return true;
       };
       auto wait_full = [&](int seq) { return wait_on(&sh.full[seq % C::kSlots], (seq / C::kSlots) & 1, sh, a.status); };
       bool ok = wait_on(&sh.q, 0, sh, a.status) && wait_full(0);
@@ -306,9 +316,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       for (int j = 0; ok && j < steps; ++j) {
         const int sv = 2 * j + 1, sk = 2 * j + 2;
         const bool more = j + 1 < steps;
-        if (!(ok = wait_full(sv) && wait_on(&sh.p[0], j & 1, sh, a.status))) break;
-        tc5_fence_after();
-        outputs(0, sv % C::kSlots, j > 0);
+        if (!(ok = wait_full(sv) && outputs(0, sv % C::kSlots, j > 0, j & 1))) break;
         if (!more) tc5_commit(smem_u32(&sh.o[0]));
         if (more) {
           if (!(ok = wait_full(sk))) break;
@@ -317,9 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tc5_commit(smem_u32(&sh.s[0]));
         }
         if (two) {
-          if (!(ok = wait_on(&sh.p[1], j & 1, sh, a.status))) break;
-          tc5_fence_after();
-          outputs(1, sv % C::kSlots, j > 0);
+          if (!(ok = outputs(1, sv % C::kSlots, j > 0, j & 1))) break;
           if (!more) tc5_commit(smem_u32(&sh.o[1]));
         }
         tc5_commit(smem_u32(&sh.empty[sv % C::kSlots]));
@@ -416,10 +422,8 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlotBytes);
           __syncwarp();
           if (lane < (kKeys >> pss)) {
-            const int y = int((int64_t(cur) * a.H_kv + h) << pss);
-#pragma unroll
-            for (int hf = 0; hf < C::kHalves; ++hf)
-              tma_load_2d(dst + hf * (kKeys * 128) + (uint32_t(lane) << (pss + 7)), part ? &tmv : &tmk, hf * 64, y, bar);
+            const int group = int(((int64_t(cur) * a.H_kv + h) << pss) >> 3);
+            tma_load_4d(dst + (uint32_t(lane * C::kGroupBytes) << (pss - 3)), part ? &tmv : &tmk, 0, 0, 0, group, bar);
           }
         } else {
           const uint8_t* pool = static_cast<const uint8_t*>(part ? a.v : a.k);
@@ -428,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll 8
           for (int r = ct / kChunks; r < kKeys; r += kCopyThreads / kChunks) {
             const int64_t off = sh.off[r];
-            cp_async_16(dst + (c >> 3) * (kKeys * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+            cp_async_16(dst + (r >> 3) * C::kGroupBytes + (c >> 3) * 1024 + (r & 7) * 128 + (((c & 7) ^ (r & 7)) << 4),
                         off >= 0 ? pool + off * (D * 2) + c * 16 : pool, off >= 0 ? 16 : 0);
           }
           cp_async_commit();
@@ -559,8 +563,7 @@ template <typename T, int D>
 sa_status dispatch(const PagedPrefillArgs& a, int splits, cudaStream_t s, const sa_cache* c, const void* q, int slot) {
   CUtensorMap mq = {}, mk = {}, mv = {};
   if (!make_query_map(&mq, q, D, a.H_q, a.T, a.G, 128 / a.G)) return SA_ERR_CUDA;
-  // a page of 8 rows and more is whole 1024-byte swizzle atoms of a slot
-  if (c->page_size >= 8 && make_pool_map(&mk, c->k, c, c->page_size) && make_pool_map(&mv, c->v, c, c->page_size))
+  if (c->page_size >= 8 && make_group_map(&mk, c->k, c, c->page_size / 8) && make_group_map(&mv, c->v, c, c->page_size / 8))
     return launch<T, D, true>(a, splits, s, mq, mk, mv, g_smem[2 * slot + 1]);
   return launch<T, D, false>(a, splits, s, mq, mk, mv, g_smem[2 * slot]);
 }
