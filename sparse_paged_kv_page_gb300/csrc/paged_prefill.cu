@@ -11,15 +11,19 @@
 // key is read once for all G heads, and walks the visible keys 128 at a time. The
 // products run on the 5th-generation tensor cores, accumulators in TMEM: S = Q K^T
 // (128 x 128, one per half), P over S's columns as the A operand from TMEM, O += P V.
-// Two warpgroups take the two halves, one row a thread (no shuffles): while one
-// turns S into P the tensor cores work for the other. One warp issues the products,
-// one the copies: keys and values in a ring of 128-row slots, page by page through
-// a tensor map (pages of 8 tokens and more), or row by row with cp.async (smaller
-// pages, and tiles with rows that must not be read: those get zeros).
+// A warpgroup takes each half, one row a thread (no shuffles): while one turns S into
+// P the tensor cores work for the other, so the time from S to P counts. One warp
+// issues the products, one the copies: keys and values in a ring of 128-row slots, page by page
+// through a tensor map (pages of 8 tokens and more), or row by row with cp.async
+// (smaller pages). Where the rows fill one half only, the halves take every other
+// step of the same rows and meet at the end.
+//
+// Value rows that no query of the CTA sees are zeroed in shared memory (a weight 0
+// times what a freed page holds must be 0), key rows masked.
 //
 // Bound by the tensor cores for prompts; for a few rows over a long cache by HBM,
-// where the keys are split over CTAs and the last of an item's CTAs merges the
-// parts in order.
+// where each item's keys are cut into parts of about the same number of steps, one
+// a CTA, and the last of an item's CTAs merges the parts in order.
 #include <type_traits>
 
 #include "common.cuh"
@@ -41,7 +45,8 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTileRing = 8;              // steps whose row masks are kept
 constexpr float kGrow = 8.0f;             // log2 of the growth of the maximum that O does not follow
-constexpr int kMaxSplit = 64;
+constexpr int kMinPart = 4;               // steps of a part at least (a part costs about two)
+constexpr int kLag = 2;                   // row-by-row copies under way behind the newest
 
 struct PagedPrefillArgs {
   const void* k;
@@ -51,11 +56,11 @@ struct PagedPrefillArgs {
   const int32_t* new_cu;
   void* out;
   float* lse;
-  float* part_o;        // [items * H_kv][splits][256][D]
-  float* part_lse;      // [items * H_kv][splits][256]
-  int32_t* tickets;     // [items * H_kv]
+  float* part_o;        // [CTAs][256][D]
+  float* part_lse;      // [CTAs][256]
+  int32_t* tickets;     // [units]
   int32_t* status;
-  int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink, items;
+  int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink, items, split;
   float scale_log2;
 };
 
@@ -67,13 +72,20 @@ struct Cfg {
   static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kQBytes = 2 * kSlotBytes;
-  static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + 1024;
+  static constexpr int kSharedAt = kQBytes + kSlots * kSlotBytes;
+};
+
+// What a CTA does: tokens [t0, t0 + nt) of request b for KV head h, steps [tb, tb + steps) of the visible keys.
+struct Work {
+  int b, item, h, part, parts, unit, c0, n, L;
 };
 
 struct Shared {
-  uint64_t full[8], empty[8], q, s[2], p[2], o[2];
+  uint64_t full[8], empty[8], q, s[2], p[2], o[2], edge;
   uint32_t tile[kTileRing][1 + kKeys / 32];   // [0]: rows of the step are masked by the words that follow
-  int64_t off[kKeys];                         // pool row of each position of a gathered step, -1: none
+  int64_t off[kKeys];                         // pool row of each position of a step copied row by row, -1: none
+  float x[2][kKeys];                          // the second half's maxima and sums, where both have the same rows
+  Work work;
   uint32_t tmem;
   int abort, last;
 };
@@ -99,6 +111,92 @@ __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared& 
   }
 }
 
+// Barriers of part of the block: 1 the copy warps, 2 the softmax warps.
+template <int kCount>
+__device__ __forceinline__ void named_sync(int id) {
+  asm volatile("bar.sync %0, %1;\n" ::"r"(id), "n"(kCount) : "memory");
+}
+template <int kCount>
+__device__ __forceinline__ bool named_any(int id, bool x) {
+  uint32_t r;
+  asm volatile("{\n .reg .pred p, q;\n setp.ne.u32 p, %3, 0;\n bar.red.or.pred q, %1, %2, p;\n selp.u32 %0, 1, 0, q;\n}\n"
+               : "=r"(r)
+               : "r"(id), "n"(kCount), "r"(uint32_t(x))
+               : "memory");
+  return r != 0;
+}
+
+// Steps of all of a request's new tokens, as its parts are cut.
+__device__ __forceinline__ int request_steps(const PagedPrefillArgs& a, int L, int n, int cap) {
+  return Span<kKeys>(L - n, L - 1, min(max(L, 0), cap), a.window, a.n_sink).tiles;
+}
+
+// The CTA's work, found by one warp. False if there is none.
+__device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Work& w) {
+  const int lane = threadIdx.x & 31, per = 2 * (128 / a.G);
+  if (!a.split) {
+    // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
+    w.h = blockIdx.x / a.items;
+    w.part = 0, w.parts = 1, w.unit = 0;
+    if (!find_item(a.new_cu, a.batch, per, a.items - 1 - blockIdx.x % a.items, w.b, w.item)) return false;
+    w.c0 = a.new_cu[w.b], w.n = a.new_cu[w.b + 1] - w.c0, w.L = a.seq_lens[w.b];
+    return true;
+  }
+  // Every (item, head) of request b in ceil(steps_b / chunk) parts, chunk the least
+  // that gives no more parts than CTAs. At most 96 requests (three a lane).
+  int c0[3], n[3], L[3], units[3], steps[3];
+  int most = 1;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int b = 32 * i + lane;
+    c0[i] = n[i] = L[i] = units[i] = steps[i] = 0;
+    if (b < a.batch) {
+      c0[i] = a.new_cu[b], n[i] = a.new_cu[b + 1] - c0[i], L[i] = a.seq_lens[b];
+      if (n[i] > 0) {
+        units[i] = (n[i] + per - 1) / per * a.H_kv;
+        steps[i] = request_steps(a, L[i], n[i], cap);
+      }
+    }
+    most = max(most, steps[i]);
+  }
+  most = __reduce_max_sync(kFull, most);
+  int lo = kMinPart, hi = max(kMinPart, most);
+  while (lo < hi) {
+    const int mid = (lo + hi) >> 1;
+    int parts = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) parts += units[i] * max(1, (steps[i] + mid - 1) / mid);
+    if (__reduce_add_sync(kFull, parts) <= int(gridDim.x)) hi = mid;
+    else lo = mid + 1;
+  }
+  int before = 0, units_before = 0;
+#pragma unroll
+  for (int i = 0; i < 3; ++i) {
+    const int np = max(1, (steps[i] + lo - 1) / lo), mine = units[i] * np;
+    int x = mine, y = units[i];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(kFull, x, o), v = __shfl_up_sync(kFull, y, o);
+      if (lane >= o) x += u, y += v;
+    }
+    const int k = __popc(__ballot_sync(kFull, before + x <= int(blockIdx.x)));
+    if (k < 32) {
+      const int first = before + __shfl_sync(kFull, x, k) - __shfl_sync(kFull, mine, k);
+      const int unit0 = units_before + __shfl_sync(kFull, y, k) - __shfl_sync(kFull, units[i], k);
+      w.parts = __shfl_sync(kFull, np, k);
+      const int at = int(blockIdx.x) - first, unit = at / w.parts;
+      w.part = at % w.parts;
+      w.unit = unit0 + unit;
+      w.h = unit % a.H_kv, w.item = unit / a.H_kv, w.b = 32 * i + k;
+      w.c0 = __shfl_sync(kFull, c0[i], k), w.n = __shfl_sync(kFull, n[i], k), w.L = __shfl_sync(kFull, L[i], k);
+      return true;
+    }
+    before += __shfl_sync(kFull, x, 31);
+    units_before += __shfl_sync(kFull, y, 31);
+  }
+  return false;
+}
+
 template <typename T, int D, bool kTma>
 __global__ void __launch_bounds__(kThreads, 1)
     paged_prefill_kernel(const __grid_constant__ PagedPrefillArgs a, const __grid_constant__ CUtensorMap tmq,
@@ -106,161 +204,205 @@ __global__ void __launch_bounds__(kThreads, 1)
   using E = Elem<T>;
   using C = Cfg<D, kTma>;
   constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
-  extern __shared__ __align__(128) uint8_t smem_raw[];
-  __shared__ Shared sh;
-  uint8_t* smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+  extern __shared__ __align__(1024) uint8_t smem[];               // Q, the ring, Shared
   uint8_t* ring = smem + C::kQBytes;
+  Shared& sh = *reinterpret_cast<Shared*>(smem + C::kSharedAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int G = a.G, pss = a.ps_shift, half_tokens = 128 / G;
-
-  // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
-  const int h = blockIdx.x / a.items, idx = a.items - 1 - blockIdx.x % a.items;
-  int b, item;
-  if (!find_item(a.new_cu, a.batch, 2 * half_tokens, idx, b, item)) return;
-  const int c0 = a.new_cu[b], n = a.new_cu[b + 1] - c0, L = a.seq_lens[b];
   const int cap = int(min(int64_t(a.bt_stride) << pss, int64_t(0x7fffffff)));
-  if (threadIdx.x == 0 && item == 0 && h == 0 && blockIdx.y == 0) {
-    if (c0 < 0 || int64_t(c0) + n > a.T || L < n) flag(a.status, SA_DEV_BAD_COUNT);
-    if (L > cap) flag(a.status, SA_DEV_OVERFLOW);
-  }
-  if (c0 < 0 || int64_t(c0) + n > a.T) return;
-  const int t0 = item * 2 * half_tokens, nt = min(2 * half_tokens, n - t0);
-  const int first = L - n + t0, last = first + nt - 1, len = min(max(L, 0), cap);
-  const Span<kKeys> sp(first, last, len, a.window, a.n_sink);
-  const bool two = nt > half_tokens;                              // the second half has rows
-  const int ns = gridDim.y, per = (sp.tiles + ns - 1) / ns;
-  const int tb = min(sp.tiles, int(blockIdx.y) * per), steps = min(sp.tiles, tb + per) - tb;
 
-  if (threadIdx.x == 0) {
+  if (warp == 0) {
+    Work w;
+    const bool any = find_work(a, cap, w);
+    if (any && w.item == 0 && w.h == 0 && w.part == 0 && lane == 0) {
+      if (w.c0 < 0 || int64_t(w.c0) + w.n > a.T || w.L < w.n) flag(a.status, SA_DEV_BAD_COUNT);
+      if (w.L > cap) flag(a.status, SA_DEV_OVERFLOW);
+    }
+    if (!any || w.c0 < 0 || int64_t(w.c0) + w.n > a.T) w.b = -1;
+    if (lane == 0) {
+      sh.work = w;
+      sh.abort = 0;
+    }
+  } else if (threadIdx.x == 32) {
     for (int i = 0; i < C::kSlots; ++i) {
       mbar_init(smem_u32(&sh.full[i]), 1);
       mbar_init(smem_u32(&sh.empty[i]), 1);
     }
     mbar_init(smem_u32(&sh.q), 1);
+    mbar_init(smem_u32(&sh.edge), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s[i]), 1);
       mbar_init(smem_u32(&sh.p[i]), 4);
       mbar_init(smem_u32(&sh.o[i]), 1);
     }
     mbar_init_fence();
-    sh.abort = 0;
+  } else if (warp == kMmaWarp) {
+    tc5_alloc(smem_u32(&sh.tmem), 512);
   }
-  if (warp == kMmaWarp) tc5_alloc(smem_u32(&sh.tmem), 512);
   tc5_fence_before();
   __syncthreads();
   tc5_fence_after();
   const uint32_t tmem = sh.tmem;                                  // columns: S/P of the halves, then O of the halves
+  const Work w = sh.work;
+  if (w.b < 0) {
+    if (warp == kMmaWarp) tc5_dealloc(tmem, 512);
+    return;
+  }
+  const int h = w.h, t0 = w.item * 2 * half_tokens, nt = min(2 * half_tokens, w.n - t0);
+  const int first = w.L - w.n + t0, last = first + nt - 1, len = min(max(w.L, 0), cap);
+  const Span<kKeys> sp(first, last, len, a.window, a.n_sink);
+  const int per = (sp.tiles + w.parts - 1) / w.parts;
+  const int tb = min(sp.tiles, w.part * per), steps = min(sp.tiles, tb + per) - tb;
+  const bool two = nt > half_tokens;                              // the second half has rows of its own
+  const bool dual = !two && steps > 1;                            // the halves take every other step of the same rows
 
   if (warp < kMmaWarp) {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
     // ------------------------------------------------------------- softmax: one row a thread
-    const int tile = warp >> 2, row = threadIdx.x & 127;
+    const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(warp & 3) << 21;              // TMEM lane 32 * (warp % 4)
-    const uint32_t s_col = tmem + lanes + tile * 128, o_col = tmem + lanes + 256 + tile * 128;
-    const int t = tile * half_tokens + row / G;
+    const uint32_t s_col = tmem + lanes + half * 128, o_col = tmem + lanes + 256 + half * 128;
+    const int t = (dual ? 0 : half * half_tokens) + row / G;
     const bool in = row / G < half_tokens && t < nt;
     const int pos = in ? first + t : -1;
-    const int64_t orow = in ? int64_t(c0 + t0 + t) * a.H_q + int64_t(h) * G + row % G : -1;
+    const int64_t orow = in ? int64_t(w.c0 + t0 + t) * a.H_q + int64_t(h) * G + row % G : -1;
     float m = -INFINITY, l = 0.f;
-    const bool act = tile == 0 || two;
-    for (int j = 0; act && j < steps; ++j) {
-      if (!__all_sync(kFull, wait_on(&sh.s[tile], j & 1, sh, a.status))) break;
+    const bool act = half == 0 || two || dual;
+    const int stride = dual ? 2 : 1;
+    uint32_t parity = 0;
+    bool ok = steps > 0;
+    for (int j = dual ? half : 0; act && j < steps; j += stride, parity ^= 1) {
+      // columns seen: up to hi, from lo on or below sk
+      const int j0 = sp.start(tb + j);
+      const int hi = min(pos, len - 1) - j0;
+      const int lo = a.window > 0 ? pos - a.window + 1 - j0 : 0, sk = a.n_sink - j0;
+      const bool cut = __any_sync(kFull, hi < kKeys - 1 || (lo > 0 && sk < kKeys));
+      ok = __all_sync(kFull, wait_on(&sh.s[half], parity, sh, a.status));
+      if (!ok) break;
       tc5_fence_after();
       float s[kKeys];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc5_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, s_col + 32 * c);
-      const int j0 = sp.start(tb + j);
-      const uint32_t* words = sh.tile[j % kTileRing];
-      const uint32_t masked = *reinterpret_cast<const volatile uint32_t*>(words);
-      // columns seen: up to hi, from lo on or below sk
-      const int hi = min(pos, len - 1) - j0;
-      const int lo = a.window > 0 ? pos - a.window + 1 - j0 : 0, sk = a.n_sink - j0;
+      const volatile uint32_t* words = sh.tile[j % kTileRing];
+      const uint32_t masked = words[0];
       tc5_wait_ld();
-      if (__any_sync(kFull, hi < kKeys - 1 || (lo > 0 && sk < kKeys) || masked)) {
+      if (cut || masked) {
+        auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
 #pragma unroll
-        for (int c = 0; c < kKeys; ++c)
-          if (c > hi || (c < lo && c >= sk)) s[c] = -INFINITY;
-        if (masked) {
+        for (int x = 0; x < 4; ++x) {
+          uint32_t see = low(hi + 1 - 32 * x) & (~low(lo - 32 * x) | low(sk - 32 * x));
+          if (masked) see &= words[1 + x];
 #pragma unroll
-          for (int w = 0; w < 4; ++w) {
-            const uint32_t bits = reinterpret_cast<const volatile uint32_t*>(words)[1 + w];
-#pragma unroll
-            for (int c = 0; c < 32; ++c)
-              if (!((bits >> c) & 1u)) s[32 * w + c] = -INFINITY;
-          }
+          for (int c = 0; c < 32; ++c) keep_if(s[32 * x + c], see, 1u << c);
         }
       }
-      float mx[4] = {s[0], s[1], s[2], s[3]};
+      auto maximum = [&]() {
+        float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-      for (int c = 4; c < kKeys - 4; c += 8) {
+        for (int c = 4; c < kKeys - 4; c += 8) {
 #pragma unroll
-        for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[c + x], s[c + 4 + x]);
-      }
+          for (int x = 0; x < 4; ++x) mx[x] = max3(mx[x], s[c + x], s[c + 4 + x]);
+        }
 #pragma unroll
-      for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[kKeys - 4 + x]);
-      const float m_new = fmaxf(m, fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-      if (j == 0) {
-        m = m_new;
-      } else if (__any_sync(kFull, (m_new - m) * a.scale_log2 > kGrow)) {
+        for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[kKeys - 4 + x]);
+        return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+      };
+      // P = 2^(scale s - scale m) to TMEM; the row's sum
+      auto weights = [&]() {
+        const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
+        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pw[16];
+#pragma unroll
+          for (int x = 0; x < 16; ++x) {
+            float p0, p1;
+            fma2(p0, p1, s[32 * c + 2 * x], s[32 * c + 2 * x + 1], a.scale_log2, base);
+            p0 = ex2_approx(p0);
+            p1 = ex2_approx(p1);
+            add2(sum[2 * (x & 1)], sum[2 * (x & 1) + 1], p0, p1);
+            pw[x] = E::pack(p0, p1);
+          }
+          tc5_st16(s_col + 16 * c, pw);
+        }
+        return (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      };
+      const float top = maximum();
+      if (j < stride) {
+        m = top;
+      } else if (__any_sync(kFull, (top - m) * a.scale_log2 > kGrow)) {
         // S of this step is complete, so the products into O before it are too
+        const float m_new = fmaxf(m, top);
         const float f = m_new == m ? 1.f : ex2_approx((m - m_new) * a.scale_log2);
         l *= f;
         m = m_new;
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          float o[32];
-          tc5_ld32(reinterpret_cast<uint32_t*>(o), o_col + 32 * c);
+        for (int c = 0; c < D / 16; ++c) {
+          float o[16];
+          tc5_ld16(reinterpret_cast<uint32_t*>(o), o_col + 16 * c);
           tc5_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 32; ++x) o[x] *= f;
-          tc5_st32(o_col + 32 * c, reinterpret_cast<uint32_t*>(o));
+          for (int x = 0; x < 16; ++x) o[x] *= f;
+          tc5_st16(o_col + 16 * c, reinterpret_cast<uint32_t*>(o));
         }
       }
-      const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
-      float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t w[16];
-#pragma unroll
-        for (int x = 0; x < 16; ++x) {
-          float p0, p1;
-          fma2(p0, p1, s[32 * c + 2 * x], s[32 * c + 2 * x + 1], a.scale_log2, base);
-          p0 = ex2_approx(p0);
-          p1 = ex2_approx(p1);
-          add2(sum[2 * (x & 1)], sum[2 * (x & 1) + 1], p0, p1);
-          w[x] = E::pack(p0, p1);
-        }
-        tc5_st16(s_col + 16 * c, w);
-      }
-      l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+      l += weights();
       tc5_wait_st();
       tc5_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.p[tile]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.p[half]));
     }
     // ------------------------------------------------------------- outputs
     if (act) {
-      bool ok = steps == 0 || wait_on(&sh.o[tile], 0, sh, a.status);
-      ok = __all_sync(kFull, ok) && steps > 0;
+      ok = ok && wait_on(&sh.o[half], 0, sh, a.status);
+      if (dual) ok = wait_on(&sh.o[half ^ 1], 0, sh, a.status) && ok;   // the ring is free: no product reads it
+      ok = __all_sync(kFull, ok);
       tc5_fence_after();
+      float* other = reinterpret_cast<float*>(ring);                      // [D columns][128 rows] of the second half
+      float f0 = 1.f, f1 = 0.f;
+      if (dual) {
+        if (half == 1) {
+#pragma unroll
+          for (int c = 0; c < D / 32; ++c) {
+            float o[32];
+            __syncwarp();
+            if (ok) tc5_ld32(reinterpret_cast<uint32_t*>(o), o_col + 32 * c);
+            tc5_wait_ld();
+#pragma unroll
+            for (int x = 0; x < 32; ++x) other[(32 * c + x) * kKeys + row] = o[x];
+          }
+          sh.x[0][row] = m;
+          sh.x[1][row] = l;
+        }
+        named_sync<kSoftmaxThreads>(2);
+        const float m1 = sh.x[0][row], l1 = sh.x[1][row], top = fmaxf(m, m1);
+        f0 = m == -INFINITY ? 0.f : ex2_approx((m - top) * a.scale_log2);
+        f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - top) * a.scale_log2);
+        l = l * f0 + l1 * f1;
+        m = top;
+      }
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const float row_lse = l > 0.f ? (m * a.scale_log2 + lg2_approx(l)) * kLn2 : -INFINITY;
-      const int64_t prow = ((int64_t(blockIdx.x) * ns + blockIdx.y) * 2 + tile) * 128 + row;
-      if (in) {
-        if (ns > 1) a.part_lse[prow] = row_lse;
+      const int64_t prow = int64_t(blockIdx.x) * 256 + (dual ? 0 : half * 128) + row;
+      if (in && !(dual && half == 1)) {
+        if (w.parts > 1) a.part_lse[prow] = row_lse;
         else if (a.lse) a.lse[orow] = row_lse;
       }
+      f0 *= inv;
+      f1 *= inv;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
+        if (dual && half == 1) break;                                     // (whole warps)
         float o[32];
         __syncwarp();
-        if (ok) {
-          tc5_ld32(reinterpret_cast<uint32_t*>(o), o_col + 32 * c);
-          tc5_wait_ld();
-        }
+        if (ok) tc5_ld32(reinterpret_cast<uint32_t*>(o), o_col + 32 * c);
+        tc5_wait_ld();
 #pragma unroll
-        for (int x = 0; x < 32; ++x) o[x] = l > 0.f ? o[x] * inv : 0.f;
-        if (in && ns > 1) {
+        for (int x = 0; x < 32; ++x) {
+          o[x] = l > 0.f ? o[x] * f0 : 0.f;
+          if (dual && l > 0.f) o[x] = fmaf(other[(32 * c + x) * kKeys + row], f1, o[x]);
+        }
+        if (in && w.parts > 1) {
           float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
 #pragma unroll
           for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
@@ -283,58 +425,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint64_t q_desc = tc5_desc(smem_u32(smem), 16, 1024);
       const uint64_t k_desc = tc5_desc(smem_u32(ring), 16, C::kGroupBytes);
       const uint64_t v_desc = tc5_desc(smem_u32(ring), 1024, C::kGroupBytes);
-      auto scores = [&](int tile, int slot) {                       // S = Q K^T
-        const uint64_t qd = q_desc + uint32_t(tile * C::kSlotBytes / 16), kd = k_desc + uint32_t(slot * C::kSlotBytes / 16);
+      auto scores = [&](int half, int slot) {                       // S = Q K^T
+        const uint64_t qd = q_desc + (dual ? 0u : uint32_t(half * C::kSlotBytes / 16));
+        const uint64_t kd = k_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t q_at = (kk >> 2) * (128 * 128) + (kk & 3) * 32, k_at = (kk >> 2) * 1024 + (kk & 3) * 32;
-          tc5_mma_ss(tmem + tile * 128, qd + q_at / 16, kd + k_at / 16, id_s, kk > 0);
+          tc5_mma_ss(tmem + half * 128, qd + q_at / 16, kd + k_at / 16, id_s, kk > 0);
         }
+        tc5_commit(smem_u32(&sh.s[half]));
       };
-      auto outputs = [&](int tile, int slot, bool add, uint32_t parity) {   // O += P V once P is there
-        if (!wait_on(&sh.p[tile], parity, sh, a.status)) return false;
+      auto outputs = [&](int half, int slot, bool add, uint32_t parity) {   // O += P V once P is there
+        if (!wait_on(&sh.p[half], parity, sh, a.status)) return false;
         tc5_fence_after();
         const uint64_t vd = v_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc5_mma_ts(tmem + 256 + tile * 128, tmem + tile * 128 + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
+          tc5_mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
                      add || kk > 0);
         return true;
       };
-      auto wait_full = [&](int seq) { return wait_on(&sh.full[seq % C::kSlots], (seq / C::kSlots) & 1, sh, a.status); };
+      auto wait_full = [&](int seq) {
+        const bool got = wait_on(&sh.full[seq % C::kSlots], (seq / C::kSlots) & 1, sh, a.status);
+        tc5_fence_after();
+        return got;
+      };
+      auto release = [&](int seq) { tc5_commit(smem_u32(&sh.empty[seq % C::kSlots])); };
+      // keys of step j are copy 2j of the ring, its values copy 2j + 1
       bool ok = wait_on(&sh.q, 0, sh, a.status) && wait_full(0);
       if (ok) {
-        tc5_fence_after();
         scores(0, 0);
-        tc5_commit(smem_u32(&sh.s[0]));
-        if (two) {
-          scores(1, 0);
-          tc5_commit(smem_u32(&sh.s[1]));
-        }
-        tc5_commit(smem_u32(&sh.empty[0]));
+        if (two) scores(1, 0);
+        release(0);
       }
-      for (int j = 0; ok && j < steps; ++j) {
-        const int sv = 2 * j + 1, sk = 2 * j + 2;
-        const bool more = j + 1 < steps;
-        if (!(ok = wait_full(sv) && outputs(0, sv % C::kSlots, j > 0, j & 1))) break;
-        if (!more) tc5_commit(smem_u32(&sh.o[0]));
-        if (more) {
-          if (!(ok = wait_full(sk))) break;
-          tc5_fence_after();
-          scores(0, sk % C::kSlots);
-          tc5_commit(smem_u32(&sh.s[0]));
-        }
-        if (two) {
-          if (!(ok = outputs(1, sv % C::kSlots, j > 0, j & 1))) break;
-          if (!more) tc5_commit(smem_u32(&sh.o[1]));
-        }
-        tc5_commit(smem_u32(&sh.empty[sv % C::kSlots]));
-        if (more) {
-          if (two) {
-            scores(1, sk % C::kSlots);
-            tc5_commit(smem_u32(&sh.s[1]));
+      if (ok && dual && (ok = wait_full(2))) {
+        scores(1, 2 % C::kSlots);
+        release(2);
+      }
+      if (dual) {
+        for (int j = 0; ok && j < steps; ++j) {
+          const int half = j & 1, sv = 2 * j + 1, sk = 2 * j + 4;
+          if (!(ok = wait_full(sv) && outputs(half, sv % C::kSlots, j > 1, (j >> 1) & 1))) break;
+          release(sv);
+          if (j + 2 >= steps) {
+            tc5_commit(smem_u32(&sh.o[half]));
+          } else if ((ok = wait_full(sk))) {
+            scores(half, sk % C::kSlots);
+            release(sk);
           }
-          tc5_commit(smem_u32(&sh.empty[sk % C::kSlots]));
+        }
+      } else {
+        for (int j = 0; ok && j < steps; ++j) {
+          const int sv = 2 * j + 1, sk = 2 * j + 2;
+          const bool more = j + 1 < steps;
+          if (!(ok = wait_full(sv) && outputs(0, sv % C::kSlots, j > 0, j & 1))) break;
+          if (!more) tc5_commit(smem_u32(&sh.o[0]));
+          if (more) {
+            if (!(ok = wait_full(sk))) break;
+            scores(0, sk % C::kSlots);
+          }
+          if (two) {
+            if (!(ok = outputs(1, sv % C::kSlots, j > 0, j & 1))) break;
+            if (!more) tc5_commit(smem_u32(&sh.o[1]));
+          }
+          release(sv);
+          if (more) {
+            if (two) scores(1, sk % C::kSlots);
+            release(sk);
+          }
         }
       }
       if (!ok) {                                                    // let what was issued finish
@@ -349,86 +507,160 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int ct = threadIdx.x - 32 * (kMmaWarp + 1);
     auto copy_sync = [&]() {
       if (C::kProducers == 1) __syncwarp();
-      else asm volatile("bar.sync 1, %0;\n" ::"n"(kCopyThreads) : "memory");
+      else named_sync<kCopyThreads>(1);
     };
     const int w0 = a.window > 0 ? max(0, first - a.window + 1) : 0;
-    const int32_t* btb = a.bt + int64_t(b) * a.bt_stride;
-    const int ps = 1 << pss;
-    if (steps > 0 && ct == 0) {
-      const uint32_t bar = smem_u32(&sh.q);
-      mbar_arrive_expect_tx(bar, uint32_t((two ? 2 : 1) * C::kHalves * G * half_tokens * 128));
-      for (int tile = 0; tile < (two ? 2 : 1); ++tile)
-        for (int hf = 0; hf < C::kHalves; ++hf)
-          tma_load_3d(smem_u32(smem) + tile * C::kSlotBytes + hf * kKeys * 128, &tmq, hf * 64, h * G,
-                      c0 + t0 + tile * half_tokens, bar);
-    }
-    // The block ids of a step through the tensor map, one a lane; -1 where there is none.
+    auto seen = [&](int p) { return p < len && (p >= w0 || p < a.n_sink); };   // by some query of the CTA
+    const int32_t* btb = a.bt + int64_t(w.b) * a.bt_stride;
+    const int ps = 1 << pss, pages = kKeys >> pss;
+    // Block ids of a step through the tensor map, one a lane; -1 where the page holds no row to be read.
     auto page_ids = [&](int j) {
       int id = -1;
-      if (kTma && j < steps) {
-        const int at = sp.start(tb + j) + (lane << pss);
-        if (lane < (kKeys >> pss) && at < len) id = btb[at >> pss];
+      if (kTma && j < steps && lane < pages) {
+        const int p = sp.start(tb + j) + (lane << pss);
+        if (p < len && (p + ps > w0 || p < a.n_sink)) {
+          id = btb[p >> pss];
+          if (id < 0 || id >= a.num_blocks) {
+            flag(a.status, SA_DEV_BAD_BLOCK);
+            id = -1;
+          }
+        }
       }
       return id;
     };
-    int pending = -1;                                              // slot whose gathered rows are still under way
-    auto finish = [&](int slot) {
+    int ids = page_ids(0);
+    if (steps > 0 && ct == 0) {
+      const uint32_t bar = smem_u32(&sh.q);
+      mbar_arrive_expect_tx(bar, uint32_t((two ? 2 : 1) * C::kHalves * G * half_tokens * 128));
+      for (int half = 0; half < (two ? 2 : 1); ++half)
+        for (int hf = 0; hf < C::kHalves; ++hf)
+          tma_load_3d(smem_u32(smem) + half * C::kSlotBytes + hf * kKeys * 128, &tmq, hf * 64, h * G,
+                      w.c0 + t0 + half * half_tokens, bar);
+    }
+    bool ok = true;
+    int seq = 0, done = 0;                                         // copies begun; row-by-row ones handed over
+    uint32_t edges = 0;
+    auto slot_at = [&](int x) { return smem_u32(ring) + (x % C::kSlots) * C::kSlotBytes; };
+    auto claim = [&]() {                                           // the ring slot of copy `seq` is free
+      if (seq >= C::kSlots)
+        ok = __all_sync(kFull, wait_on(&sh.empty[seq % C::kSlots], (seq / C::kSlots - 1) & 1, sh, a.status));
+      if constexpr (!kTma) ok = !named_any<kCopyThreads>(1, !ok);
+      return ok;
+    };
+    auto hand_over = [&](int x) {                                  // generic writes to the slot of copy x are complete
       fence_proxy_async_smem();
       copy_sync();
-      if (ct == 0) mbar_arrive(smem_u32(&sh.full[slot]));
+      if (ct == 0) mbar_arrive(smem_u32(&sh.full[x % C::kSlots]));
     };
-    int ids = page_ids(0);
-    bool ok = true;
-    int seq = 0;
-    for (int j = 0; ok && j < steps; ++j) {
-      const int j0 = sp.start(tb + j);
-      const int cur = ids;
-      ids = page_ids(j + 1);
-      // every row of the step may be read, and comes from a page that exists
-      bool clean = false;
-      if (kTma) {
-        clean = j0 + kKeys <= len && (j0 >= w0 || j0 + kKeys <= a.n_sink);
-        clean = clean && __all_sync(kFull, lane >= (kKeys >> pss) || (cur >= 0 && cur < a.num_blocks));
+    if constexpr (kTma) {
+      int edge_seq = -1;                                           // values whose unseen rows are still to be zeroed
+      uint32_t edge_bits[4];
+      auto finish_edge = [&]() {
+        if (edge_seq < 0) return;
+        ok = __all_sync(kFull, wait_on(&sh.edge, edges++ & 1, sh, a.status));
+        if (!ok) return;
+        constexpr int kChunks = D / 8;
+        const int c = lane % kChunks;
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          if (edge_bits[x] == 0xffffffffu) continue;
+          for (int r = lane / kChunks; r < 32; r += 32 / kChunks)
+            if (!((edge_bits[x] >> r) & 1u))
+              asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};\n" ::"r"(
+                               slot_at(edge_seq) + (4 * x + (r >> 3)) * C::kGroupBytes + (c >> 3) * 1024 + (r & 7) * 128 +
+                               (c & 7) * 16),
+                           "r"(0u)
+                           : "memory");
+        }
+        hand_over(edge_seq);
+        edge_seq = -1;
+      };
+      for (int j = 0; ok && j < steps; ++j) {
+        const int j0 = sp.start(tb + j), cur = ids;
+        ids = page_ids(j + 1);
+        const uint32_t have = __ballot_sync(kFull, cur >= 0);
+        const bool clean = __popc(have) == pages && j0 + kKeys <= len && (j0 >= w0 || j0 + kKeys <= a.n_sink);
+        uint32_t bits[4];
+        if (!clean) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            const int r = 32 * x + lane;
+            bits[x] = __ballot_sync(kFull, seen(j0 + r) && ((have >> (r >> pss)) & 1u));
+            if (lane == 0) sh.tile[j % kTileRing][1 + x] = bits[x];
+          }
+        }
+        if (lane == 0) sh.tile[j % kTileRing][0] = !clean;
+        __syncwarp();
+        const uint32_t bytes = __popc(have) * (uint32_t(C::kGroupBytes) << pss >> 3);
+        const int group = int(((int64_t(max(cur, 0)) * a.H_kv + h) << pss) >> 3);
+        auto copy = [&](const CUtensorMap& map, uint32_t bar) {
+          if (lane == 0) mbar_arrive_expect_tx(bar, bytes);
+          __syncwarp();
+          if (cur >= 0)
+            tma_load_4d(slot_at(seq) + (uint32_t(lane * C::kGroupBytes) << pss >> 3), &map, 0, 0, 0, group, bar);
+          ++seq;
+        };
+        if (!claim()) break;
+        copy(tmk, smem_u32(&sh.full[seq % C::kSlots]));
+        finish_edge();
+        if (!ok || !claim()) break;
+        if (clean) {
+          copy(tmv, smem_u32(&sh.full[seq % C::kSlots]));
+        } else {
+          edge_seq = seq;
+#pragma unroll
+          for (int x = 0; x < 4; ++x) edge_bits[x] = bits[x];
+          fence_proxy_async_smem();
+          copy(tmv, smem_u32(&sh.edge));
+        }
       }
-      if (!clean) {
-        copy_sync();                                               // the offsets of the step before are used up
-        for (int r0 = 0; r0 < kKeys; r0 += kCopyThreads) {
-          const int r = r0 + ct, p = j0 + r;
-          if (r >= kKeys) break;                                   // (whole warps)
-          int64_t off = -1;
-          if (p < len && (p >= w0 || p < a.n_sink)) {
+      const int left = edge_seq;
+      if (ok) finish_edge();
+      if (!ok) {                                                   // leave no copy under way (bounded waits)
+        mbar_wait(smem_u32(&sh.q), 0, a.status);
+        for (int x = max(0, seq - C::kSlots); x < seq; ++x)
+          if (x != left) mbar_wait(smem_u32(&sh.full[x % C::kSlots]), (x / C::kSlots) & 1, a.status);
+      }
+    } else {
+      // pool rows of a step's positions, two at most a thread, looked up a step ahead
+      auto look_up = [&](int j, int64_t (&off)[2]) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = i * kCopyThreads + ct, p = sp.start(tb + j) + r;
+          off[i] = -1;
+          if (j < steps && r < kKeys && seen(p)) {
             const int blk = btb[p >> pss];
             if (blk < 0 || blk >= a.num_blocks) flag(a.status, SA_DEV_BAD_BLOCK);
-            else off = ((int64_t(blk) * a.H_kv + h) << pss) + (p & (ps - 1));
+            else off[i] = ((int64_t(blk) * a.H_kv + h) << pss) + (p & (ps - 1));
           }
-          sh.off[r] = off;
-          const uint32_t bits = __ballot_sync(kFull, off >= 0);
+        }
+      };
+      int64_t next[2];
+      look_up(0, next);
+      for (int j = 0; ok && j < steps; ++j) {
+        copy_sync();                                               // the rows of the step before are used up
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          const int r = i * kCopyThreads + ct;
+          if (r >= kKeys) break;                                   // (whole warps)
+          sh.off[r] = next[i];
+          const uint32_t bits = __ballot_sync(kFull, next[i] >= 0);
           if (lane == 0) sh.tile[j % kTileRing][1 + r / 32] = bits;
         }
-      }
-      if (ct == 0) sh.tile[j % kTileRing][0] = !clean;
-      copy_sync();
-#pragma unroll 1
-      for (int part = 0; part < 2; ++part, ++seq) {
-        const int slot = seq % C::kSlots;
-        if (seq >= C::kSlots) {
-          ok = wait_on(&sh.empty[slot], (seq / C::kSlots - 1) & 1, sh, a.status);
-          ok = __all_sync(kFull, ok);
-          if (!ok) break;
+        look_up(j + 1, next);
+        copy_sync();
+        if (ct == 0) {
+          uint32_t all = 0xffffffffu;
+          for (int x = 0; x < 4; ++x) all &= sh.tile[j % kTileRing][1 + x];
+          sh.tile[j % kTileRing][0] = all != 0xffffffffu;
         }
-        const uint32_t dst = smem_u32(ring) + slot * C::kSlotBytes;
-        if (clean) {
-          const uint32_t bar = smem_u32(&sh.full[slot]);
-          if (lane == 0) mbar_arrive_expect_tx(bar, C::kSlotBytes);
-          __syncwarp();
-          if (lane < (kKeys >> pss)) {
-            const int group = int(((int64_t(cur) * a.H_kv + h) << pss) >> 3);
-            tma_load_4d(dst + (uint32_t(lane * C::kGroupBytes) << (pss - 3)), part ? &tmv : &tmk, 0, 0, 0, group, bar);
-          }
-        } else {
+#pragma unroll 1
+        for (int part = 0; part < 2; ++part) {
+          if (!claim()) break;
           const uint8_t* pool = static_cast<const uint8_t*>(part ? a.v : a.k);
           constexpr int kChunks = D / 8;
           const int c = ct % kChunks;
+          const uint32_t dst = slot_at(seq);
 #pragma unroll 8
           for (int r = ct / kChunks; r < kKeys; r += kCopyThreads / kChunks) {
             const int64_t off = sh.off[r];
@@ -436,25 +668,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                         off >= 0 ? pool + off * (D * 2) + c * 16 : pool, off >= 0 ? 16 : 0);
           }
           cp_async_commit();
-          if (kTma) {
-            cp_async_wait<0>();
-            finish(slot);
-          } else {
-            if (pending >= 0) {
-              cp_async_wait<1>();
-              finish(pending);
-            }
-            pending = slot;
+          ++seq;
+          if (seq - done > kLag) {
+            cp_async_wait<kLag>();
+            hand_over(done++);
           }
         }
       }
-    }
-    cp_async_wait<0>();
-    if (pending >= 0) finish(pending);
-    if (!ok && steps > 0) {                                        // leave no copy under way (bounded waits)
-      mbar_wait(smem_u32(&sh.q), 0, a.status);
-      for (int x = max(0, seq - C::kSlots); x < seq; ++x)
-        mbar_wait(smem_u32(&sh.full[x % C::kSlots]), (x / C::kSlots) & 1, a.status);
+      cp_async_wait<0>();
+      while (done < seq) hand_over(done++);
+      if (!ok && ct == 0) mbar_wait(smem_u32(&sh.q), 0, a.status);
     }
   }
   }
@@ -463,58 +686,55 @@ __global__ void __launch_bounds__(kThreads, 1)
     tc5_fence_after();
     tc5_dealloc(tmem, 512);
   }
-  if (ns == 1 || warp >= kMmaWarp) return;
+  if (w.parts == 1 || warp >= kMmaWarp) return;
 
-  // ------------------------------------------------------------- merge the parts of the item
-  auto merge_sync = [] { asm volatile("bar.sync 2, %0;\n" ::"n"(kSoftmaxThreads) : "memory"); };
-  if (threadIdx.x == 0) sh.last = ticket(&a.tickets[blockIdx.x]) == ns - 1;
-  merge_sync();
+  // ------------------------------------------------------------- merge the parts of the unit
+  if (threadIdx.x == 0) sh.last = ticket(&a.tickets[w.unit]) == w.parts - 1;
+  named_sync<kSoftmaxThreads>(2);
   if (!sh.last) return;
-  float* wgt = reinterpret_cast<float*>(smem);                     // [256][ns], then 1 / sum in [256]
-  float* inv = wgt + 256 * ns;
-  const int64_t part0 = int64_t(blockIdx.x) * ns * 256;
-  auto row_of = [&](int r) -> int64_t {                            // row of q and out, -1: none
-    const int t = (r >> 7) * half_tokens + (r & 127) / G;
-    if ((r & 127) / G >= half_tokens || t >= nt) return -1;
-    return int64_t(c0 + t0 + t) * a.H_q + int64_t(h) * G + (r & 127) % G;
-  };
-  const int mine = threadIdx.x;
-  if (const int64_t orow = row_of(mine); orow >= 0) {
-    const int r = mine;
-    float M = -INFINITY, tot = 0.f;
-    for (int s = 0; s < ns; ++s) {
-      const float x = __ldcg(a.part_lse + part0 + s * 256 + r);
-      wgt[r * ns + s] = x;
-      M = fmaxf(M, x);
-    }
-    for (int s = 0; s < ns; ++s) {
-      const float x = wgt[r * ns + s], w = x == -INFINITY ? 0.f : ex2_approx((x - M) * kLog2e);
-      wgt[r * ns + s] = w;
-      tot += w;
-    }
-    inv[r] = tot > 0.f ? 1.0f / tot : 0.f;
-    if (a.lse) a.lse[orow] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
-  }
-  merge_sync();
-  for (int i = threadIdx.x; i < 256 * (D / 4); i += kSoftmaxThreads) {
+  const int64_t part0 = (int64_t(blockIdx.x) - w.part) * 256;
+  const int rows = two ? 256 : 128;
+  for (int i = threadIdx.x; i < rows * (D / 4); i += kSoftmaxThreads) {
+    // a thread merges four columns of a row, four parts in flight, in the order of the parts
     const int r = i / (D / 4), d = 4 * (i % (D / 4));
-    const int64_t orow = row_of(r);
-    if (orow < 0) continue;
+    const int t = (r >> 7) * half_tokens + (r & 127) / G;
+    if ((r & 127) / G >= half_tokens || t >= nt) continue;
+    const int64_t orow = int64_t(w.c0 + t0 + t) * a.H_q + int64_t(h) * G + (r & 127) % G;
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int s = 0; s < ns; ++s) {
-      const float w = wgt[r * ns + s];
-      const float4 x = __ldcg(reinterpret_cast<const float4*>(a.part_o + (part0 + s * 256 + r) * D + d));
-      acc.x = fmaf(w, x.x, acc.x);
-      acc.y = fmaf(w, x.y, acc.y);
-      acc.z = fmaf(w, x.z, acc.z);
-      acc.w = fmaf(w, x.w, acc.w);
+    float M = -INFINITY, tot = 0.f;
+    for (int p0 = 0; p0 < w.parts; p0 += 4) {
+      float4 x[4];
+      float z[4];
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        z[k] = -INFINITY;
+        if (p0 + k < w.parts) {
+          const int64_t at = part0 + (p0 + k) * 256 + r;
+          z[k] = __ldcg(a.part_lse + at);
+          x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d));
+        }
+      }
+      const float top = fmaxf(M, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
+      const float f = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLog2e);
+      tot *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+      M = top;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (z[k] == -INFINITY) continue;                           // an empty part
+        const float g = ex2_approx((z[k] - M) * kLog2e);
+        tot += g;
+        acc.x = fmaf(g, x[k].x, acc.x);
+        acc.y = fmaf(g, x[k].y, acc.y);
+        acc.z = fmaf(g, x[k].z, acc.z);
+        acc.w = fmaf(g, x[k].w, acc.w);
+      }
     }
-    const float f = inv[r];
+    const float f = tot > 0.f ? 1.0f / tot : 0.f;
     *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + d) =
         make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
+    if (a.lse && d == 0) a.lse[orow] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
   }
-  if (threadIdx.x == 0) a.tickets[blockIdx.x] = 0;
+  if (threadIdx.x == 0) a.tickets[w.unit] = 0;
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
@@ -522,22 +742,13 @@ size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 // Items of a call: at most one partly filled one per request.
 int64_t items_of(int64_t tokens, int batch, int G) { return tokens / (2 * (128 / G)) + batch; }
 
-// CTAs that share an item's keys: as many as fill the SMs once, where the items
-// alone would leave half of them idle.
-int splits_of(int64_t ctas, int64_t cap_tokens, int sms) {
-  if (2 * ctas > sms) return 1;
-  int64_t s = sms / ctas;
-  const int64_t steps = (cap_tokens + kKeys - 1) / kKeys;
-  if (s > steps) s = steps;
-  if (s > kMaxSplit) s = kMaxSplit;
-  return s < 1 ? 1 : int(s);
-}
+// Items are cut into parts where they would leave half of the SMs idle (three
+// requests a lane are looked over then).
+bool splits(int64_t units, int batch, int sms) { return 2 * units <= sms && batch <= 96; }
 
 struct WsLayout {
   size_t part_lse, part_o, total;
 };
-// For `ctas` (item, split) pairs. Where a call splits, items x splits <= SMs, so
-// this depends on the call's tokens only through whether it can split at all.
 WsLayout ws_layout(int64_t ctas, int D) {
   WsLayout w;
   w.part_lse = align256(size_t(ctas) * 4);
@@ -549,23 +760,24 @@ WsLayout ws_layout(int64_t ctas, int D) {
 int g_smem[8][64];
 
 template <typename T, int D, bool kTma>
-sa_status launch(const PagedPrefillArgs& a, int splits, cudaStream_t s, const CUtensorMap& mq, const CUtensorMap& mk,
+sa_status launch(const PagedPrefillArgs& a, cudaStream_t s, const CUtensorMap& mq, const CUtensorMap& mk,
                  const CUtensorMap& mv, int* cache) {
   auto k = paged_prefill_kernel<T, D, kTma>;
-  if (!ensure_smem(k, Cfg<D, kTma>::kSmem, cache)) return SA_ERR_CUDA;
-  return launch_ex(k, dim3(unsigned(a.items) * a.H_kv, splits), dim3(kThreads), Cfg<D, kTma>::kSmem, s,
-                   false, 1, a, mq, mk, mv) == cudaSuccess
+  constexpr int smem = Cfg<D, kTma>::kSharedAt + int(sizeof(Shared));
+  if (!ensure_smem(k, smem, cache)) return SA_ERR_CUDA;
+  const unsigned ctas = a.split ? unsigned(sm_count()) : unsigned(a.items) * a.H_kv;
+  return launch_ex(k, dim3(ctas), dim3(kThreads), smem, s, false, 1, a, mq, mk, mv) == cudaSuccess
              ? SA_OK
              : SA_ERR_CUDA;
 }
 
 template <typename T, int D>
-sa_status dispatch(const PagedPrefillArgs& a, int splits, cudaStream_t s, const sa_cache* c, const void* q, int slot) {
+sa_status dispatch(const PagedPrefillArgs& a, cudaStream_t s, const sa_cache* c, const void* q, int slot) {
   CUtensorMap mq = {}, mk = {}, mv = {};
   if (!make_query_map(&mq, q, D, a.H_q, a.T, a.G, 128 / a.G)) return SA_ERR_CUDA;
   if (c->page_size >= 8 && make_group_map(&mk, c->k, c, c->page_size / 8) && make_group_map(&mv, c->v, c, c->page_size / 8))
-    return launch<T, D, true>(a, splits, s, mq, mk, mv, g_smem[2 * slot + 1]);
-  return launch<T, D, false>(a, splits, s, mq, mk, mv, g_smem[2 * slot]);
+    return launch<T, D, true>(a, s, mq, mk, mv, g_smem[2 * slot + 1]);
+  return launch<T, D, false>(a, s, mq, mk, mv, g_smem[2 * slot]);
 }
 
 }  // namespace
@@ -577,8 +789,8 @@ extern "C" size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_
   if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_tokens < 0 ||
       num_q_heads % num_kv_heads)
     return 0;
-  const int64_t least = int64_t(batch) * num_kv_heads;             // items of a call of few tokens
-  return 2 * least > sm_count() ? 256 : ws_layout(sm_count(), head_dim).total;
+  // a call of few tokens has an item per request: what it needs, calls of more tokens need at most
+  return splits(int64_t(batch) * num_kv_heads, batch, sm_count()) ? ws_layout(sm_count(), head_dim).total : 256;
 }
 
 extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
@@ -604,13 +816,11 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
   a.H_kv = H; a.H_q = num_q_heads; a.G = G; a.ps_shift = log2i(cache->page_size); a.num_blocks = cache->num_blocks;
   a.bt_stride = batch->bt_stride; a.batch = batch->batch; a.T = num_tokens; a.window = window; a.n_sink = n_sink;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf(float(D))) * kLog2e;
-  const int64_t items = items_of(num_tokens, batch->batch, G), ctas = items * H;
-  if (ctas > 0x7fffffff) return SA_ERR_UNSUPPORTED;
+  const int64_t items = items_of(num_tokens, batch->batch, G), units = items * H;
+  if (units > 0x7fffffff) return SA_ERR_UNSUPPORTED;
   a.items = int(items);
-  const int64_t seen = window > 0 ? int64_t(window) + n_sink + 3 * kKeys : int64_t(1) << 40;
-  const int64_t cap = int64_t(batch->bt_stride) * cache->page_size;
-  const int splits = splits_of(ctas, cap < seen ? cap : seen, sm_count());
-  if (splits > 1) {
+  a.split = splits(units, batch->batch, sm_count());
+  if (a.split) {
     const WsLayout w = ws_layout(sm_count(), D);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.tickets = reinterpret_cast<int32_t*>(ws);
@@ -620,6 +830,6 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SA_BF16;
   if (D == 128)
-    return bf ? dispatch<__nv_bfloat16, 128>(a, splits, s, cache, q, 0) : dispatch<__half, 128>(a, splits, s, cache, q, 1);
-  return bf ? dispatch<__nv_bfloat16, 64>(a, splits, s, cache, q, 2) : dispatch<__half, 64>(a, splits, s, cache, q, 3);
+    return bf ? dispatch<__nv_bfloat16, 128>(a, s, cache, q, 0) : dispatch<__half, 128>(a, s, cache, q, 1);
+  return bf ? dispatch<__nv_bfloat16, 64>(a, s, cache, q, 2) : dispatch<__half, 64>(a, s, cache, q, 3);
 }
