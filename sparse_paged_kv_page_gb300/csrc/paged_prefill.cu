@@ -2,10 +2,9 @@
 // one, a few drafted tokens) over the paged cache that already holds them.
 //
 // Mathematics: o = sum_j p_j v_j, p = softmax(scale q . k_j) over the visible
-// positions j, in one pass with a running maximum m and sum l. O is rescaled only
-// where m has grown by more than 2^8 since it was last used (p stays below 2^8,
-// exact in float32 sums and inside both 16-bit types); the quotient o / l at the
-// end makes any m right.
+// positions j, in one pass with a running reference m near the maximum and the sum l;
+// O and l are rescaled only where the weights 2^(scale (s - m)) have grown large; the
+// quotient o / l at the end makes any m right.
 //
 // A CTA owns 2 x 128 packed rows (token, query head of one KV head's group), so a
 // key is read once for all G heads, and walks the visible keys 128 at a time. The
@@ -44,7 +43,11 @@ constexpr int kThreads = kSoftmaxThreads + 128;
 // 256 x 208 + 128 x 88 = 384 x 168.
 constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTileRing = 8;              // steps whose row masks are kept
-constexpr float kGrow = 8.0f;             // log2 of the growth of the maximum that O does not follow
+// The running maximum m follows the row only when a step's sum of weights 2^(scale (s - m)) passes this: below it
+// every weight is inside both 16-bit types, and float32 sums do not mind. So no step but the first looks for its
+// maximum (60 instructions of 380 a row), the sum that is made anyway tells.
+constexpr float kMostSum = 8192.0f;
+constexpr int kRun = 8;                   // words of P stored at a time
 constexpr int kMinPart = 4;               // steps of a part at least (a part costs about two)
 constexpr int kLag = 2;                   // row-by-row copies under way behind the newest
 
@@ -72,6 +75,11 @@ struct Cfg {
   static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
   static constexpr int kSlots = D == 128 ? 5 : 8;
   static constexpr int kQBytes = 2 * kSlotBytes;
+  // TMEM columns: S of the halves, O of the halves, and at D = 64, where there is room, P apart from S, so that the
+  // next step's S is made while this one's P is (sliding-window prompts 189 -> 179 us); at D = 128 P overwrites S.
+  static constexpr bool kApart = D == 64;
+  static constexpr int kOCol = 256, kPCol = kApart ? 384 : 0;
+  static constexpr int kPStride = kApart ? 64 : 128;
   static constexpr int kSharedAt = kQBytes + kSlots * kSlotBytes;
 };
 
@@ -81,29 +89,30 @@ struct Work {
 };
 
 struct Shared {
-  uint64_t full[8], empty[8], q, s[2], p[2], o[2], edge;
+  // of the halves: s made, s read (r), p made, products of a step complete (v; r and v where P is apart), the last ones (o)
+  uint64_t full[8], empty[8], q, s[2], r[2], p[2], v[2], o[2], edge, drain;
   uint32_t tile[kTileRing][1 + kKeys / 32];   // [0]: rows of the step are masked by the words that follow
   int64_t off[kKeys];                         // pool row of each position of a step copied row by row, -1: none
   float x[2][kKeys];                          // the second half's maxima and sums, where both have the same rows
   Work work;
   uint32_t tmem;
-  int abort, last;
+  int abort, last, bad;                       // bad: a page that was to be read has no block
 };
 
 // Wait for a phase; false once any wait of the CTA has given up. The clock is read
 // only after many tries (each try suspends the thread for a while by itself).
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Shared& sh, int32_t* status) {
   const uint32_t b = smem_u32(bar);
+  if (mbar_try_wait(b, parity)) return true;
+  uint64_t t0 = 0;
 #pragma unroll 1
-  for (int i = 0; i < 256; ++i)
+  for (uint32_t i = 1;; ++i) {
     if (mbar_try_wait(b, parity)) return true;
-  const uint64_t t0 = global_ns();
-  while (true) {
-#pragma unroll 1
-    for (int i = 0; i < 64; ++i)
-      if (mbar_try_wait(b, parity)) return true;
+    if (i & 63) continue;
     if (*reinterpret_cast<volatile int*>(&sh.abort)) return false;
-    if (global_ns() - t0 > kWaitLimitNs) {
+    const uint64_t t = global_ns();
+    if (!t0) t0 = t;
+    if (t - t0 > kWaitLimitNs) {
       flag(status, SA_DEV_TIMEOUT);
       *reinterpret_cast<volatile int*>(&sh.abort) = 1;
       return false;
@@ -222,6 +231,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 0) {
       sh.work = w;
       sh.abort = 0;
+      sh.bad = 0;
     }
   } else if (threadIdx.x == 32) {
     for (int i = 0; i < C::kSlots; ++i) {
@@ -230,10 +240,13 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mbar_init(smem_u32(&sh.q), 1);
     mbar_init(smem_u32(&sh.edge), 1);
+    mbar_init(smem_u32(&sh.drain), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s[i]), 1);
       mbar_init(smem_u32(&sh.p[i]), 4);
       mbar_init(smem_u32(&sh.o[i]), 1);
+      mbar_init(smem_u32(&sh.r[i]), 4);
+      mbar_init(smem_u32(&sh.v[i]), 1);
     }
     mbar_init_fence();
   } else if (warp == kMmaWarp) {
@@ -261,41 +274,51 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ------------------------------------------------------------- softmax: one row a thread
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(warp & 3) << 21;              // TMEM lane 32 * (warp % 4)
-    const uint32_t s_col = tmem + lanes + half * 128, o_col = tmem + lanes + 256 + half * 128;
+    const uint32_t s_col = tmem + lanes + half * 128, o_col = tmem + lanes + C::kOCol + half * D;
+    const uint32_t p_col = tmem + lanes + C::kPCol + half * C::kPStride;
     const int t = (dual ? 0 : half * half_tokens) + row / G;
     const bool in = row / G < half_tokens && t < nt;
     const int pos = in ? first + t : -1;
     const int64_t orow = in ? int64_t(w.c0 + t0 + t) * a.H_q + int64_t(h) * G + row % G : -1;
-    float m = -INFINITY, l = 0.f;
+    float m = in ? -INFINITY : 0.f, l = 0.f;                      // m: -inf until the row has seen a key
     const bool act = half == 0 || two || dual;
     const int stride = dual ? 2 : 1;
     uint32_t parity = 0;
     bool ok = steps > 0;
+    // the warp's rows: steps that end behind `low`, or begin before `high`'s window, hide keys from one of them
+    const int low = __reduce_min_sync(kFull, in ? min(pos, len - 1) : 0x7fffffff);
+    const int high = __reduce_max_sync(kFull, pos);
     for (int j = dual ? half : 0; act && j < steps; j += stride, parity ^= 1) {
-      // columns seen: up to hi, from lo on or below sk
       const int j0 = sp.start(tb + j);
-      const int hi = min(pos, len - 1) - j0;
-      const int lo = a.window > 0 ? pos - a.window + 1 - j0 : 0, sk = a.n_sink - j0;
-      const bool cut = __any_sync(kFull, hi < kKeys - 1 || (lo > 0 && sk < kKeys));
-      ok = __all_sync(kFull, wait_on(&sh.s[half], parity, sh, a.status));
-      if (!ok) break;
+      const bool cut = j0 + kKeys - 1 > low || (a.window > 0 && j0 <= high - a.window && j0 + kKeys > a.n_sink);
+      ok = wait_on(&sh.s[half], parity, sh, a.status) && ok;       // (a wait that gave up: the rest runs on to its end)
+      __syncwarp();
       tc5_fence_after();
       float s[kKeys];
 #pragma unroll
       for (int c = 0; c < 4; ++c) tc5_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, s_col + 32 * c);
-      const volatile uint32_t* words = sh.tile[j % kTileRing];
-      const uint32_t masked = words[0];
+      const int bad = *reinterpret_cast<volatile int*>(&sh.bad);   // looked at with the sum below
       tc5_wait_ld();
-      if (cut || masked) {
-        auto low = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
+      if constexpr (C::kApart) {
+        tc5_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&sh.r[half]));
+      }
+      auto hide = [&]() {
+        // columns seen: up to hi, from lo on or below sk, and those whose rows the step has
+        const int hi = min(pos, len - 1) - j0;
+        const int lo = a.window > 0 ? pos - a.window + 1 - j0 : 0, sk = a.n_sink - j0;
+        const volatile uint32_t* words = sh.tile[j % kTileRing];
+        const bool some = words[0];
+        auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? 0xffffffffu : (1u << n) - 1u; };
 #pragma unroll
         for (int x = 0; x < 4; ++x) {
-          uint32_t see = low(hi + 1 - 32 * x) & (~low(lo - 32 * x) | low(sk - 32 * x));
-          if (masked) see &= words[1 + x];
+          uint32_t see = below(hi + 1 - 32 * x) & (~below(lo - 32 * x) | below(sk - 32 * x));
+          if (some) see &= words[1 + x];
 #pragma unroll
           for (int c = 0; c < 32; ++c) keep_if(s[32 * x + c], see, 1u << c);
         }
-      }
+      };
       auto maximum = [&]() {
         float mx[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
@@ -307,46 +330,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[kKeys - 4 + x]);
         return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       };
-      // P = 2^(scale s - scale m) to TMEM; the row's sum
-      auto weights = [&]() {
+      // P = 2^(scale s - scale m) to TMEM, eight words at a time and one run behind; the row's sum
+      auto weights = [&](bool wait_p) {
         const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
         float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        uint32_t pw[2][kRun];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pw[16];
+        for (int c = 0; c <= 64 / kRun; ++c) {
+          if (c < 64 / kRun) {
 #pragma unroll
-          for (int x = 0; x < 16; ++x) {
-            float p0, p1;
-            fma2(p0, p1, s[32 * c + 2 * x], s[32 * c + 2 * x + 1], a.scale_log2, base);
-            p0 = ex2_approx(p0);
-            p1 = ex2_approx(p1);
-            add2(sum[2 * (x & 1)], sum[2 * (x & 1) + 1], p0, p1);
-            pw[x] = E::pack(p0, p1);
+            for (int x = 0; x < kRun; ++x) {
+              float p0, p1;
+              fma2(p0, p1, s[2 * kRun * c + 2 * x], s[2 * kRun * c + 2 * x + 1], a.scale_log2, base);
+              p0 = ex2_approx(p0);
+              p1 = ex2_approx(p1);
+              add2(sum[2 * (x & 1)], sum[2 * (x & 1) + 1], p0, p1);
+              pw[c & 1][x] = E::pack(p0, p1);
+            }
           }
-          tc5_st16(s_col + 16 * c, pw);
+          if (c == 1 && wait_p) {
+            // the products of the step before have read P
+            ok = wait_on(&sh.v[half], parity ^ 1, sh, a.status) && ok;
+            __syncwarp();
+            tc5_fence_after();
+          }
+          if (c > 0) tc5_st8(p_col + kRun * (c - 1), pw[(c - 1) & 1]);
         }
         return (sum[0] + sum[1]) + (sum[2] + sum[3]);
       };
-      const float top = maximum();
-      if (j < stride) {
-        m = top;
-      } else if (__any_sync(kFull, (top - m) * a.scale_log2 > kGrow)) {
-        // S of this step is complete, so the products into O before it are too
-        const float m_new = fmaxf(m, top);
+      if (cut) hide();
+      if (j < stride && in) m = maximum();
+      float sum = weights(C::kApart && j >= stride);
+      if (__any_sync(kFull, (in && (!(sum <= kMostSum) || m == -INFINITY)) || bad)) {
+        // some row's maximum has grown: O and l follow it, and P is made again (it has not been handed over)
+        if (bad) hide();
+        const float m_new = in ? fmaxf(m, maximum()) : m;
         const float f = m_new == m ? 1.f : ex2_approx((m - m_new) * a.scale_log2);
         l *= f;
         m = m_new;
+        if (j >= stride) {
+          // the products into O before this step are complete
 #pragma unroll
-        for (int c = 0; c < D / 16; ++c) {
-          float o[16];
-          tc5_ld16(reinterpret_cast<uint32_t*>(o), o_col + 16 * c);
-          tc5_wait_ld();
+          for (int c = 0; c < D / 16; ++c) {
+            float o[16];
+            tc5_ld16(reinterpret_cast<uint32_t*>(o), o_col + 16 * c);
+            tc5_wait_ld();
 #pragma unroll
-          for (int x = 0; x < 16; ++x) o[x] *= f;
-          tc5_st16(o_col + 16 * c, reinterpret_cast<uint32_t*>(o));
+            for (int x = 0; x < 16; ++x) o[x] *= f;
+            tc5_st16(o_col + 16 * c, reinterpret_cast<uint32_t*>(o));
+          }
         }
+        sum = weights(false);
       }
-      l += weights();
+      l += sum;
       tc5_wait_st();
       tc5_fence_before();
       __syncwarp();
@@ -441,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t vd = v_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc5_mma_ts(tmem + 256 + half * 128, tmem + half * 128 + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
+          tc5_mma_ts(tmem + C::kOCol + half * D, tmem + C::kPCol + half * C::kPStride + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
                      add || kk > 0);
         return true;
       };
@@ -462,14 +498,30 @@ __global__ void __launch_bounds__(kThreads, 1)
         scores(1, 2 % C::kSlots);
         release(2);
       }
+      // S of the next step of a half, once the half has read the one before (P apart)
+      auto ahead = [&](int half, int seq, uint32_t parity) {
+        if (!wait_full(seq) || !wait_on(&sh.r[half], parity, sh, a.status)) return false;
+        tc5_fence_after();
+        scores(half, seq % C::kSlots);
+        return true;
+      };
+      auto done = [&](int half, bool more) {
+        if (!more) tc5_commit(smem_u32(&sh.o[half]));
+        else if (C::kApart) tc5_commit(smem_u32(&sh.v[half]));
+      };
       if (dual) {
         for (int j = 0; ok && j < steps; ++j) {
           const int half = j & 1, sv = 2 * j + 1, sk = 2 * j + 4;
-          if (!(ok = wait_full(sv) && outputs(half, sv % C::kSlots, j > 1, (j >> 1) & 1))) break;
+          const uint32_t parity = (j >> 1) & 1;
+          const bool more = j + 2 < steps;
+          if (C::kApart && more) {
+            if (!(ok = ahead(half, sk, parity))) break;
+            release(sk);
+          }
+          if (!(ok = wait_full(sv) && outputs(half, sv % C::kSlots, j > 1, parity))) break;
           release(sv);
-          if (j + 2 >= steps) {
-            tc5_commit(smem_u32(&sh.o[half]));
-          } else if ((ok = wait_full(sk))) {
+          done(half, more);
+          if (!C::kApart && more && (ok = wait_full(sk))) {
             scores(half, sk % C::kSlots);
             release(sk);
           }
@@ -478,26 +530,27 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int j = 0; ok && j < steps; ++j) {
           const int sv = 2 * j + 1, sk = 2 * j + 2;
           const bool more = j + 1 < steps;
-          if (!(ok = wait_full(sv) && outputs(0, sv % C::kSlots, j > 0, j & 1))) break;
-          if (!more) tc5_commit(smem_u32(&sh.o[0]));
-          if (more) {
-            if (!(ok = wait_full(sk))) break;
-            scores(0, sk % C::kSlots);
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            if (half && !two) break;
+            if (C::kApart && more && !(ok = ahead(half, sk, j & 1))) break;
+            if (half == 0 && !(ok = wait_full(sv))) break;
+            if (!(ok = outputs(half, sv % C::kSlots, j > 0, j & 1))) break;
+            done(half, more);
+            if (!C::kApart && more) {
+              if (half == 1 || !two) release(sv);
+              if (half == 0 && !(ok = wait_full(sk))) break;
+              scores(half, sk % C::kSlots);
+            }
           }
-          if (two) {
-            if (!(ok = outputs(1, sv % C::kSlots, j > 0, j & 1))) break;
-            if (!more) tc5_commit(smem_u32(&sh.o[1]));
-          }
-          release(sv);
-          if (more) {
-            if (two) scores(1, sk % C::kSlots);
-            release(sk);
-          }
+          if (!ok) break;
+          if (C::kApart || !more) release(sv);
+          if (more) release(sk);
         }
       }
       if (!ok) {                                                    // let what was issued finish
-        tc5_commit(smem_u32(&sh.o[0]));
-        mbar_wait(smem_u32(&sh.o[0]), 0, a.status);
+        tc5_commit(smem_u32(&sh.drain));
+        mbar_wait(smem_u32(&sh.drain), 0, a.status);
       }
     }
     __syncwarp();
@@ -522,6 +575,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           id = btb[p >> pss];
           if (id < 0 || id >= a.num_blocks) {
             flag(a.status, SA_DEV_BAD_BLOCK);
+            *reinterpret_cast<volatile int*>(&sh.bad) = 1;
             id = -1;
           }
         }
@@ -630,8 +684,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           off[i] = -1;
           if (j < steps && r < kKeys && seen(p)) {
             const int blk = btb[p >> pss];
-            if (blk < 0 || blk >= a.num_blocks) flag(a.status, SA_DEV_BAD_BLOCK);
-            else off[i] = ((int64_t(blk) * a.H_kv + h) << pss) + (p & (ps - 1));
+            if (blk < 0 || blk >= a.num_blocks) {
+              flag(a.status, SA_DEV_BAD_BLOCK);
+              *reinterpret_cast<volatile int*>(&sh.bad) = 1;
+            } else {
+              off[i] = ((int64_t(blk) * a.H_kv + h) << pss) + (p & (ps - 1));
+            }
           }
         }
       };
