@@ -59,16 +59,21 @@ __device__ __forceinline__ void tma_load_4d(uint32_t dst, const void* tmap, int 
       : "memory");
 }
 
+__device__ __forceinline__ void prefetch_map(const void* tmap) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(tmap)) : "memory");
+}
+
 // Work item `idx` of a ragged batch in which request b has ceil(n_b / per) items
-// (n_b = new_cu[b+1] - new_cu[b]): its request and its place there. All lanes of
-// a warp call it. False behind the last item.
-__device__ __forceinline__ bool find_item(const int32_t* new_cu, int batch, int per, int idx, int& b, int& i) {
+// (n_b = new_cu[b+1] - new_cu[b]): its request, its place there, the request's first
+// row, rows and length. All lanes of a warp call it. False behind the last item.
+__device__ __forceinline__ bool find_item(const int32_t* new_cu, const int32_t* seq_lens, int batch, int per, int idx,
+                                          int& b, int& i, int& c0, int& n, int& L) {
   const int lane = threadIdx.x & 31;
   int before = 0;
   for (int b0 = 0; b0 < batch; b0 += 32) {
-    const bool in = b0 + lane < batch;
-    const int n = in ? new_cu[b0 + lane + 1] - new_cu[b0 + lane] : 0;
-    const int items = n > 0 ? (n + per - 1) / per : 0;
+    const int at = min(b0 + lane, batch - 1);
+    const int first = new_cu[at], rows = b0 + lane < batch ? new_cu[at + 1] - first : 0, len = seq_lens[at];
+    const int items = rows > 0 ? (rows + per - 1) / per : 0;
     int x = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -79,6 +84,7 @@ __device__ __forceinline__ bool find_item(const int32_t* new_cu, int batch, int 
     if (k < 32) {
       i = idx - before - (__shfl_sync(kFull, x, k) - __shfl_sync(kFull, items, k));
       b = b0 + k;
+      c0 = __shfl_sync(kFull, first, k), n = __shfl_sync(kFull, rows, k), L = __shfl_sync(kFull, len, k);
       return true;
     }
     before += __shfl_sync(kFull, x, 31);

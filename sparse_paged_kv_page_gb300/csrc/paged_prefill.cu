@@ -147,9 +147,7 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Wo
     // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
     w.h = blockIdx.x / a.items;
     w.part = 0, w.parts = 1, w.unit = 0;
-    if (!find_item(a.new_cu, a.batch, per, a.items - 1 - blockIdx.x % a.items, w.b, w.item)) return false;
-    w.c0 = a.new_cu[w.b], w.n = a.new_cu[w.b + 1] - w.c0, w.L = a.seq_lens[w.b];
-    return true;
+    return find_item(a.new_cu, a.seq_lens, a.batch, per, a.items - 1 - blockIdx.x % a.items, w.b, w.item, w.c0, w.n, w.L);
   }
   // Every (item, head) of request b in ceil(steps_b / chunk) parts, chunk the least
   // that gives no more parts than CTAs. At most 96 requests (three a lane).
@@ -251,6 +249,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init_fence();
   } else if (warp == kMmaWarp) {
     tc5_alloc(smem_u32(&sh.tmem), 512);
+  } else if (threadIdx.x == kSoftmaxThreads + 32) {
+    prefetch_map(&tmq);
+    if (kTma) {
+      prefetch_map(&tmk);
+      prefetch_map(&tmv);
+    }
   }
   tc5_fence_before();
   __syncthreads();
@@ -426,6 +430,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       f0 *= inv;
       f1 *= inv;
+      uint8_t* stage = smem + half * C::kSlotBytes + row * (D * 2);
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         if (dual && half == 1) break;                                     // (whole warps)
@@ -438,16 +443,33 @@ __global__ void __launch_bounds__(kThreads, 1)
           o[x] = l > 0.f ? o[x] * f0 : 0.f;
           if (dual && l > 0.f) o[x] = fmaf(other[(32 * c + x) * kKeys + row], f1, o[x]);
         }
-        if (in && w.parts > 1) {
-          float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+        if (w.parts > 1) {
+          if (in) {
+            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
 #pragma unroll
-          for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
-        } else if (in) {
-          uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow * D + 32 * c);
+            for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+          }
+        } else {
+          // through the half's query rows in shared memory (every product with them is complete), so that a store
+          // instruction covers whole rows of out and not 16 bytes of 32 of them
 #pragma unroll
           for (int x = 0; x < 4; ++x)
-            dst[x] = make_uint4(E::pack(o[8 * x], o[8 * x + 1]), E::pack(o[8 * x + 2], o[8 * x + 3]),
-                                E::pack(o[8 * x + 4], o[8 * x + 5]), E::pack(o[8 * x + 6], o[8 * x + 7]));
+            *reinterpret_cast<uint4*>(stage + ((4 * c + x) ^ (row & 7)) * 16) =
+                make_uint4(E::pack(o[8 * x], o[8 * x + 1]), E::pack(o[8 * x + 2], o[8 * x + 3]),
+                           E::pack(o[8 * x + 4], o[8 * x + 5]), E::pack(o[8 * x + 6], o[8 * x + 7]));
+        }
+      }
+      if (w.parts == 1 && !(dual && half == 1)) {
+        __syncwarp();
+        constexpr int kChunks = D / 8, kRows = 32 / kChunks;               // 16-byte chunks of a row, rows at a time
+        const int chunk = lane % kChunks;
+        uint8_t* rows = stage - lane * (D * 2);
+#pragma unroll 4
+        for (int r0 = 0; r0 < 32; r0 += kRows) {
+          const int r = r0 + lane / kChunks;
+          const int64_t to = __shfl_sync(kFull, orow, r);
+          const uint4 x = *reinterpret_cast<const uint4*>(rows + r * (D * 2) + (chunk ^ (r & 7)) * 16);
+          if (to >= 0) *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + to * D + chunk * 8) = x;
         }
       }
       tc5_fence_before();
@@ -582,7 +604,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       return id;
     };
-    int ids = page_ids(0);
     if (steps > 0 && ct == 0) {
       const uint32_t bar = smem_u32(&sh.q);
       mbar_arrive_expect_tx(bar, uint32_t((two ? 2 : 1) * C::kHalves * G * half_tokens * 128));
@@ -591,6 +612,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(smem_u32(smem) + half * C::kSlotBytes + hf * kKeys * 128, &tmq, hf * 64, h * G,
                       w.c0 + t0 + half * half_tokens, bar);
     }
+    int ids = page_ids(0);
     bool ok = true;
     int seq = 0, done = 0;                                         // copies begun; row-by-row ones handed over
     uint32_t edges = 0;
