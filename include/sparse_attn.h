@@ -664,7 +664,8 @@ size_t sa_paged_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32
  *   j <= i and (window == 0 or j > i - window or j < n_sink):
  * the whole cache, or the `window` most recent tokens, itself included, and the
  * n_sink first ones. An empty request gives out = 0, lse = -inf.
- *   q, out   [batch, num_q_heads, head_dim], dtype; 16-byte aligned
+ *   q, out   [batch, num_q_heads, head_dim], dtype; 16-byte aligned; out may be
+ *            q itself
  *   scale    <= 0 selects head_dim ** -0.5
  *   lse      nullable float32 [batch, num_q_heads], natural log
  * Tokens that the query does not see are never used, whatever they hold. Pages
@@ -689,8 +690,9 @@ size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_heads, int3
  * Request b's queries are rows new_cu[b] .. new_cu[b+1]-1 of q, at positions
  * seq_lens[b] - n_b .. seq_lens[b] - 1; each sees what sa_paged_decode's query
  * at its position sees. Prompts, chunks of prompts and a few drafted tokens.
- *   q, out   [num_tokens, num_q_heads, head_dim], dtype; 16-byte aligned; rows
- *            from new_cu[batch] on are padding: neither read nor written
+ *   q, out   [num_tokens, num_q_heads, head_dim], dtype; 16-byte aligned; out
+ *            may be q itself; rows from new_cu[batch] on are padding: never
+ *            used, never written
  *   new_cu   [batch + 1] int32, device, non-decreasing, new_cu[0] = 0
  *   lse      nullable float32 [num_tokens, num_q_heads], natural log
  * A request whose rows leave [0, num_tokens] sets SA_DEV_BAD_COUNT and is

@@ -442,21 +442,21 @@ def make_rope(table: Optional[torch.Tensor], *, interleaved: bool = False,
     return r
 
 
-def _rows(t, name: str, dtype, heads: int, head_dim: int):
-    """Address and token stride of rows [T, heads, head_dim] whose tokens may lie apart (heads 0: any)."""
-    shape = t.shape
-    if t.dtype != dtype or not t.is_cuda or len(shape) != 3 or shape[2] != head_dim or (heads and shape[1] != heads):
-        raise ValueError(f"{name} must be a CUDA tensor [T, {heads or 'heads'}, {head_dim}] of the cache dtype {dtype}")
+def _rows(t, name: str, dtype, device: int, T: int, heads: int, head_dim: int):
+    """Address and token stride of rows [T, heads, head_dim] on `device` whose tokens may lie apart."""
+    if t.dtype is not dtype or t.get_device() != device or t.shape != (T, heads, head_dim):
+        raise ValueError(f"{name} must be [{T}, {heads}, {head_dim}] of {dtype} on device {device}, got "
+                         f"{tuple(t.shape)} of {t.dtype} on {t.device}")
     stride, head, one = t.stride()
-    if one != 1 or (head != head_dim and shape[1] > 1):
+    if one != 1 or (head != head_dim and heads > 1):
         raise ValueError(f"the heads of a token of {name} must be contiguous")
-    return t.data_ptr(), stride if shape[0] > 1 else max(stride, shape[1] * head_dim)
+    return t.data_ptr(), stride if T > 1 else heads * head_dim
 
 
-def _whole(t, dtype, name: str):
-    """_p of a tensor that is there, in fewer steps."""
-    if t.dtype != dtype or not t.is_contiguous() or not t.is_cuda:
-        raise ValueError(f"{name} must be a contiguous CUDA tensor of {dtype}")
+def _whole(t, dtype, device: int, name: str):
+    """Address of a contiguous tensor on `device`."""
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous tensor of {dtype} on device {device}")
     return t.data_ptr()
 
 
@@ -488,24 +488,19 @@ def sa_append_kv_rope(cache: SaCache, batch: SaBatch, rope: SaRope, q, k_new, v_
     append of k_new and v_new. Tokens may lie apart (slices of one projection's output). advanced: the
     batch's lengths already count the new tokens and stay as they are."""
     pool = cache._keep[0]
-    dt = pool.dtype
+    dt, dev = pool.dtype, pool.get_device()
     _, H, _, D = pool.shape
     T = k_new.shape[0]
-    kp, ks = _rows(k_new, "k_new", dt, H, D)
-    vp, vs = _rows(v_new, "v_new", dt, H, D)
-    if v_new.shape[0] != T:
-        raise ValueError("q, k_new and v_new must have the same tokens")
+    kp, ks = _rows(k_new, "k_new", dt, dev, T, H, D)
+    vp, vs = _rows(v_new, "v_new", dt, dev, T, H, D)
     qp = qop = None
     qs = hq = 0
     if q is not None:
-        qp, qs = _rows(q, "q", dt, 0, D)
-        shape = q.shape
-        hq = shape[1]
-        if shape[0] != T:
-            raise ValueError("q, k_new and v_new must have the same tokens")
-        if q_out is None or q_out.shape != shape:
+        hq = q.shape[1] if q.dim() == 3 else 0
+        qp, qs = _rows(q, "q", dt, dev, T, hq, D)
+        if q_out is None or q_out.shape != q.shape:
             raise ValueError("q_out must be like q")
-        qop = _whole(q_out, dt, "q_out")
+        qop = _whole(q_out, dt, dev, "q_out")
     elif q_out is not None:
         raise ValueError("q_out without q")
     if new_cu.numel() != batch.batch + 1:
@@ -513,16 +508,17 @@ def sa_append_kv_rope(cache: SaCache, batch: SaBatch, rope: SaRope, q, k_new, v_
     _, positions, qw, kw = rope._keep
     if positions is not None and positions.shape[-1] != T:
         raise ValueError("positions must have one column for each row of k_new")
-    for w in (qw, kw):
-        if w is not None and (w.dtype != dt or w.numel() != D):
-            raise ValueError("q_weight and k_weight must be [head_dim] in the cache dtype")
-    _launch("sa_append_kv_rope", pool.get_device(), stream, ctypes.addressof(cache), ctypes.addressof(batch),
-            ctypes.addressof(rope), qp, qs, hq, kp, ks, vp, vs, _whole(new_cu, torch.int32, "new_cu"), T,
+    if qw is not None and (qw.dtype is not dt or qw.numel() != D):
+        raise ValueError("q_weight must be [head_dim] in the cache dtype")
+    if kw is not None and (kw.dtype is not dt or kw.numel() != D):
+        raise ValueError("k_weight must be [head_dim] in the cache dtype")
+    _launch("sa_append_kv_rope", dev, stream, ctypes.addressof(cache), ctypes.addressof(batch),
+            ctypes.addressof(rope), qp, qs, hq, kp, ks, vp, vs, _whole(new_cu, torch.int32, dev, "new_cu"), T,
             max_new_per_req, 1 if advanced else 0, qop,
-            None if hh is None else _whole(hh, torch.bfloat16, "hh"),
-            None if ret_pos is None else _whole(ret_pos, torch.int32, "ret_pos"),
-            None if ret_cnt is None else _whole(ret_cnt, torch.int32, "ret_cnt"), ret_cap,
-            None if dev_status is None else _whole(dev_status, torch.int32, "dev_status"))
+            None if hh is None else _whole(hh, torch.bfloat16, dev, "hh"),
+            None if ret_pos is None else _whole(ret_pos, torch.int32, dev, "ret_pos"),
+            None if ret_cnt is None else _whole(ret_cnt, torch.int32, dev, "ret_cnt"), ret_cap,
+            None if dev_status is None else _whole(dev_status, torch.int32, dev, "dev_status"))
 
 
 def sa_paged_decode_workspace_size(batch: int, num_kv_heads: int, num_q_heads: int, head_dim: int) -> int:
@@ -553,7 +549,7 @@ def alloc_paged_prefill_workspace(batch, num_kv_heads, num_q_heads, head_dim, nu
 def _attention(cache, q, num_q_heads, out, lse, workspace):
     """Addresses of the rows of an attention call, checked: q, out, lse, workspace and its bytes, and the device."""
     pool = cache._keep[0]
-    dt, shape = pool.dtype, q.shape
+    dt, dev, shape = pool.dtype, pool.get_device(), q.shape
     if len(shape) != 3 or shape[1] != num_q_heads or shape[2] != pool.shape[3]:
         raise ValueError(f"q must be [rows, {num_q_heads}, {pool.shape[3]}], got {tuple(shape)}")
     if out.shape != shape:
@@ -563,10 +559,10 @@ def _attention(cache, q, num_q_heads, out, lse, workspace):
     if lse is not None:
         if lse.shape != shape[:2]:
             raise ValueError("lse must be [rows, num_q_heads]")
-        lp = _whole(lse, torch.float32, "lse")
+        lp = _whole(lse, torch.float32, dev, "lse")
     if workspace is not None:
-        wp, wbytes = _p(workspace, name="workspace"), workspace.nbytes
-    return _whole(q, dt, "q"), _whole(out, dt, "out"), lp, wp, wbytes, pool.get_device()
+        wp, wbytes = _whole(workspace, workspace.dtype, dev, "workspace"), workspace.nbytes
+    return _whole(q, dt, dev, "q"), _whole(out, dt, dev, "out"), lp, wp, wbytes, dev
 
 
 def sa_paged_decode(cache: SaCache, batch: SaBatch, q, num_q_heads: int, scale: float, out, window: int = 0,
@@ -578,7 +574,7 @@ def sa_paged_decode(cache: SaCache, batch: SaBatch, q, num_q_heads: int, scale: 
         raise ValueError("q must have one row for each request")
     _launch("sa_paged_decode", device, stream, ctypes.addressof(cache), ctypes.addressof(batch), qp, num_q_heads,
             window, n_sink, scale, op, lp, wp, wbytes,
-            None if dev_status is None else _whole(dev_status, torch.int32, "dev_status"))
+            None if dev_status is None else _whole(dev_status, torch.int32, device, "dev_status"))
 
 
 def sa_paged_prefill(cache: SaCache, batch: SaBatch, q, num_q_heads: int, new_cu, scale: float, out,
@@ -589,5 +585,5 @@ def sa_paged_prefill(cache: SaCache, batch: SaBatch, q, num_q_heads: int, new_cu
     if new_cu.numel() != batch.batch + 1:
         raise ValueError("new_cu must be [batch + 1]")
     _launch("sa_paged_prefill", device, stream, ctypes.addressof(cache), ctypes.addressof(batch), qp, num_q_heads,
-            _whole(new_cu, torch.int32, "new_cu"), q.shape[0], window, n_sink, scale, op, lp, wp, wbytes,
-            None if dev_status is None else _whole(dev_status, torch.int32, "dev_status"))
+            _whole(new_cu, torch.int32, device, "new_cu"), q.shape[0], window, n_sink, scale, op, lp, wp, wbytes,
+            None if dev_status is None else _whole(dev_status, torch.int32, device, "dev_status"))

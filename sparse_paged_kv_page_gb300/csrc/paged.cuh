@@ -70,24 +70,32 @@ __device__ __forceinline__ bool find_item(const int32_t* new_cu, const int32_t* 
                                           int& b, int& i, int& c0, int& n, int& L) {
   const int lane = threadIdx.x & 31;
   int before = 0;
-  for (int b0 = 0; b0 < batch; b0 += 32) {
-    const int at = min(b0 + lane, batch - 1);
-    const int first = new_cu[at], rows = b0 + lane < batch ? new_cu[at + 1] - first : 0, len = seq_lens[at];
-    const int items = rows > 0 ? (rows + per - 1) / per : 0;
-    int x = items;
+  for (int b0 = 0; b0 < batch; b0 += 128) {            // 128 requests a round of loads
+    int first[4], rows[4], len[4];
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int y = __shfl_up_sync(kFull, x, o);
-      if (lane >= o) x += y;
+    for (int j = 0; j < 4; ++j) {
+      const int at = min(b0 + 32 * j + lane, batch - 1);
+      first[j] = new_cu[at], rows[j] = new_cu[at + 1] - first[j], len[j] = seq_lens[at];
+      if (b0 + 32 * j + lane >= batch) rows[j] = 0;
     }
-    const int k = __popc(__ballot_sync(kFull, before + x <= idx));
-    if (k < 32) {
-      i = idx - before - (__shfl_sync(kFull, x, k) - __shfl_sync(kFull, items, k));
-      b = b0 + k;
-      c0 = __shfl_sync(kFull, first, k), n = __shfl_sync(kFull, rows, k), L = __shfl_sync(kFull, len, k);
-      return true;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int items = rows[j] > 0 ? (rows[j] + per - 1) / per : 0;
+      int x = items;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int y = __shfl_up_sync(kFull, x, o);
+        if (lane >= o) x += y;
+      }
+      const int k = __popc(__ballot_sync(kFull, before + x <= idx));
+      if (k < 32) {
+        i = idx - before - (__shfl_sync(kFull, x, k) - __shfl_sync(kFull, items, k));
+        b = b0 + 32 * j + k;
+        c0 = __shfl_sync(kFull, first[j], k), n = __shfl_sync(kFull, rows[j], k), L = __shfl_sync(kFull, len[j], k);
+        return true;
+      }
+      before += __shfl_sync(kFull, x, 31);
     }
-    before += __shfl_sync(kFull, x, 31);
   }
   return false;
 }

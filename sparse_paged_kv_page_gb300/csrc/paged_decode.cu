@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   };
   const int head_groups = groups_of(0);          // of requests 0 .. 31
   int all = head_groups;
+#pragma unroll 4
   for (int b0 = 32; b0 < a.batch; b0 += 32) all += groups_of(b0);
   const int64_t total = __reduce_add_sync(kFull, all), N = min(int64_t(gridDim.x), total);   // every CTA has a group
   if (blockIdx.x >= N) return;
@@ -519,7 +520,8 @@ extern "C" sa_status sa_paged_decode(const sa_cache* cache, const sa_batch* batc
   a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
   a.part_o = reinterpret_cast<float*>(ws + w.part_o);
   a.H_kv = H; a.H_q = num_q_heads; a.G = G; a.ps_shift = log2i(cache->page_size); a.num_blocks = cache->num_blocks;
-  a.bt_stride = batch->bt_stride; a.batch = batch->batch; a.window = window; a.n_sink = n_sink;
+  a.bt_stride = batch->bt_stride; a.batch = batch->batch; a.n_sink = n_sink;
+  a.window = window < cap ? window : 0;                      // a window of the table's length hides nothing
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf(float(D))) * kLog2e;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SA_BF16;

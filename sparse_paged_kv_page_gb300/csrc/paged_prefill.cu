@@ -894,7 +894,9 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
   a.k = cache->k; a.v = cache->v; a.bt = batch->block_table; a.seq_lens = batch->seq_lens; a.new_cu = new_cu;
   a.out = out; a.lse = lse; a.status = dev_status;
   a.H_kv = H; a.H_q = num_q_heads; a.G = G; a.ps_shift = log2i(cache->page_size); a.num_blocks = cache->num_blocks;
-  a.bt_stride = batch->bt_stride; a.batch = batch->batch; a.T = num_tokens; a.window = window; a.n_sink = n_sink;
+  a.bt_stride = batch->bt_stride; a.batch = batch->batch; a.T = num_tokens; a.n_sink = n_sink;
+  // a window of the table's length hides nothing
+  a.window = window < int64_t(batch->bt_stride) * cache->page_size ? window : 0;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf(float(D))) * kLog2e;
   const int64_t items = items_of(num_tokens, batch->batch, G), units = items * H;
   if (units > 0x7fffffff) return SA_ERR_UNSUPPORTED;

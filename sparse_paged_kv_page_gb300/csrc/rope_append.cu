@@ -449,8 +449,12 @@ __device__ __forceinline__ void query_unit(const RopeArgs& a, int u) {
   load_positions(a, t, pos);
   const Row<NP> w = weights(ln, a.q_weight);
   // the token's request: the first whose rows end behind t
-  int b = 0, c0 = 0, c1 = 0, L = 0;
-  for (int b0 = 0; b0 < a.batch; b0 += 32) {
+  int b = 0, c0 = 0, c1 = 0, L = 0, from = 0;
+  if (a.batch > 32) {                        // first among 32 evenly spaced ones: two rounds of loads for 1024 requests
+    const int step = (a.batch + 31) / 32;
+    from = step * __popc(__ballot_sync(kFull, a.new_cu[min((lane + 1) * step, a.batch)] <= t));
+  }
+  for (int b0 = from; b0 < a.batch; b0 += 32) {
     const int i = min(b0 + lane, a.batch - 1);
     const int end = a.new_cu[i + 1], beg = a.new_cu[i], len = a.seq_lens[i];
     const int k = __popc(__ballot_sync(kFull, b0 + lane < a.batch && end <= t));

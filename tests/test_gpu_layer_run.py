@@ -207,6 +207,62 @@ def test_two_graphs_share_a_workspace_in_order():
     assert torch.equal(o[0], o[2]) and torch.equal(o[1], o[3])
 
 
+def test_outputs_over_the_queries_and_first_calls_captured():
+    p = Problem([700, 64, 3], Hkv=1, G=4, D=64, ps=8, dtype="fp16")
+    S = p.S
+    cu = torch.tensor([0, 300, 301, 304], dtype=torch.int32).cuda()
+    qd, qp = p.rand(3, 4, 64), p.rand(304, 4, 64)
+    od, op = torch.empty_like(qd), torch.empty_like(qp)
+    wd, wp = S.alloc_paged_decode_workspace(3, 1, 4, 64), S.alloc_paged_prefill_workspace(3, 1, 4, 64, 304)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        S.sa_paged_decode(p.cache, p.batch, qd, 4, 0.0, od, workspace=wd)
+        S.sa_paged_prefill(p.cache, p.batch, qp, 4, cu, 0.0, op, workspace=wp)
+    g.replay()
+    S.sa_paged_decode(p.cache, p.batch, qd, 4, 0.0, qd, workspace=wd)
+    S.sa_paged_prefill(p.cache, p.batch, qp, 4, cu, 0.0, qp, workspace=wp)
+    torch.cuda.synchronize()
+    assert torch.equal(od, qd) and torch.equal(op, qp)
+
+
+def test_windows_as_long_as_the_cache_hide_nothing():
+    p = Problem([500, 1], Hkv=2, G=2)
+    S = p.S
+    q = p.rand(2, 4, 128)
+    cu = torch.tensor([0, 1, 2], dtype=torch.int32).cuda()
+    ws = S.alloc_paged_decode_workspace(2, 2, 4, 128), S.alloc_paged_prefill_workspace(2, 2, 4, 128, 2)
+    for window in (500, 2 ** 31 - 1):
+        o = [torch.empty_like(q) for _ in range(4)]
+        for i, w in ((0, 0), (1, window)):
+            S.sa_paged_decode(p.cache, p.batch, q, 4, 0.0, o[i], window=w, n_sink=i, workspace=ws[0])
+            S.sa_paged_prefill(p.cache, p.batch, q, 4, cu, 0.0, o[2 + i], window=w, n_sink=i, workspace=ws[1])
+        torch.cuda.synchronize()
+        assert torch.equal(o[0], o[1]) and torch.equal(o[2], o[3])
+
+
+def test_a_thousand_requests():
+    lens = [(17 * i) % 61 for i in range(1000)]
+    new = [1 + i % 3 for i in range(1000)]
+    p = Problem([a + b for a, b in zip(lens, new)], Hkv=1, G=2, D=64)
+    S, T = p.S, sum(new)
+    cu = torch.tensor([0] + new).cumsum(0).to(torch.int32).cuda()
+    q, out = p.rand(T, 2, 64), torch.empty((T, 2, 64), dtype=p.dt, device="cuda")
+    lse = torch.empty((T, 2), device="cuda")
+    S.sa_paged_prefill(p.cache, p.batch, q, 2, cu, 0.0, out, lse=lse, dev_status=p.status,
+                       workspace=S.alloc_paged_prefill_workspace(1000, 1, 2, 64, T))
+    last = q[cu[1:].long() - 1].contiguous()
+    od, ld = torch.empty_like(last), torch.empty((1000, 2), device="cuda")
+    S.sa_paged_decode(p.cache, p.batch, last, 2, 0.0, od, lse=ld, dev_status=p.status,
+                      workspace=S.alloc_paged_decode_workspace(1000, 1, 2, 64))
+    torch.cuda.synchronize()
+    assert int(p.status) == 0
+    for b in list(range(0, 1000, 37)) + [999]:
+        L, n, r = p.lens[b], new[b], slice(int(cu[b]), int(cu[b + 1]))
+        want = attention64(q[r], *p.seqs[b], torch.arange(L - n, L, device="cuda"), 0.125, 0, 0)
+        check_attention(out[r], lse[r], want)
+        check_attention(od[b:b + 1], ld[b:b + 1], [x[-1:] for x in want])
+
+
 def test_binding_refuses_other_shapes_and_types():
     p = Problem([20], Hkv=2, G=2, meta=True)
     S = p.S
