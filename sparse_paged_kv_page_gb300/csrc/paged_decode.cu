@@ -32,6 +32,7 @@ constexpr int kThreads = kWarps * 32;
 constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxBatch = 1024;
+constexpr int kFlight = 8;                 // parts a merging thread has in flight
 
 struct PagedDecodeArgs {
   const void* k;
@@ -403,17 +404,20 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       if (threadIdx.x == 0) s_last = ticket(&a.tickets[unit]) == parts - 1;
       __syncthreads();
       if (s_last) {
-        // a thread merges four columns of a row, eight parts in flight, in the order of the parts
+        // A thread merges four columns of a row, kFlight parts in flight, in the order of the parts; where the rows
+        // leave threads over, `ways` of them take every ways-th batch of a column and meet in shared memory.
         auto slot_of = [&](int p) { return 2 * int64_t(c_first + p) + (p == 0 ? 1 : 0); };
-        for (int idx = 4 * threadIdx.x; idx < G * D; idx += 4 * kThreads) {
-          const int row = idx / D;
+        const int quads = G * (D / 4), ways = quads >= kThreads ? 1 : kThreads / quads;
+        float* meet = reinterpret_cast<float*>(smem);        // [ways][quads][6]
+        for (int i = threadIdx.x; i < quads * ways; i += kThreads) {
+          const int quad = i % quads, way = i / quads, idx = 4 * quad, row = idx / D;
           float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
           float M = -INFINITY, tot = 0.f;
-          for (int p0 = 0; p0 < parts; p0 += 8) {
-            float4 x[8];
-            float z[8];
+          for (int p0 = way * kFlight; p0 < parts; p0 += ways * kFlight) {
+            float4 x[kFlight];
+            float z[kFlight];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kFlight; ++k) {
               z[k] = -INFINITY;
               if (p0 + k < parts) {
                 const int64_t r = slot_of(p0 + k) * G;
@@ -423,12 +427,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             }
             float m = M;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) m = fmaxf(m, z[k]);
+            for (int k = 0; k < kFlight; ++k) m = fmaxf(m, z[k]);
             const float f = M == -INFINITY ? 0.f : ex2_approx((M - m) * kLog2e);
             tot *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
             M = m;
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
+            for (int k = 0; k < kFlight; ++k) {
               if (z[k] == -INFINITY) continue;             // an empty part
               const float w = ex2_approx((z[k] - M) * kLog2e);
               tot += w;
@@ -438,9 +442,35 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               acc.w = fmaf(w, x[k].w, acc.w);
             }
           }
+          if (ways > 1) {
+            float* mine = meet + int64_t(i) * 6;
+            mine[0] = M, mine[1] = tot, mine[2] = acc.x, mine[3] = acc.y, mine[4] = acc.z, mine[5] = acc.w;
+            continue;
+          }
           const float f = tot > 0.f ? 1.0f / tot : 0.f;
           *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
           if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+        }
+        if (ways > 1) {
+          __syncthreads();
+          if (int(threadIdx.x) < quads) {
+            const int idx = 4 * threadIdx.x, row = idx / D;
+            float M = -INFINITY, tot = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < ways; ++q) M = fmaxf(M, meet[(q * quads + threadIdx.x) * 6]);
+            for (int q = 0; q < ways; ++q) {
+              const float* x = meet + (q * quads + threadIdx.x) * 6;
+              const float w = x[0] == -INFINITY ? 0.f : ex2_approx((x[0] - M) * kLog2e);
+              tot = fmaf(w, x[1], tot);
+              acc.x = fmaf(w, x[2], acc.x);
+              acc.y = fmaf(w, x[3], acc.y);
+              acc.z = fmaf(w, x[4], acc.z);
+              acc.w = fmaf(w, x[5], acc.w);
+            }
+            const float f = tot > 0.f ? 1.0f / tot : 0.f;
+            *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
+            if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+          }
         }
         if (threadIdx.x == 0) a.tickets[unit] = 0;
       }

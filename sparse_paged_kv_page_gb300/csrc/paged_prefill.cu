@@ -135,9 +135,9 @@ __device__ __forceinline__ bool named_any(int id, bool x) {
   return r != 0;
 }
 
-// Steps of all of a request's new tokens, as its parts are cut.
-__device__ __forceinline__ int request_steps(const PagedPrefillArgs& a, int L, int n, int cap) {
-  return Span<kKeys>(L - n, L - 1, min(max(L, 0), cap), a.window, a.n_sink).tiles;
+// Steps of a request's last item of `per` tokens, which has the most, as its items' parts are cut.
+__device__ __forceinline__ int request_steps(const PagedPrefillArgs& a, int L, int n, int per, int cap) {
+  return Span<kKeys>(L - min(n, per), L - 1, min(max(L, 0), cap), a.window, a.n_sink).tiles;
 }
 
 // The CTA's work, found by one warp. False if there is none.
@@ -161,7 +161,7 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Wo
       c0[i] = a.new_cu[b], n[i] = a.new_cu[b + 1] - c0[i], L[i] = a.seq_lens[b];
       if (n[i] > 0) {
         units[i] = (n[i] + per - 1) / per * a.H_kv;
-        steps[i] = request_steps(a, L[i], n[i], cap);
+        steps[i] = request_steps(a, L[i], n[i], per, cap);
       }
     }
     most = max(most, steps[i]);

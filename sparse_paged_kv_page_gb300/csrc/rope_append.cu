@@ -29,12 +29,12 @@ constexpr int kKeyPairs = 4, kQueryPairs = 8;   // pairs of columns of a lane
 constexpr int kQueryBatch = 2;                  // rows of queries a lane has in flight beside those at work
 
 // Calls whose warps fit the SMs at once wait for loads: many rows in flight a lane,
-// three blocks an SM. Others need warps: six blocks an SM. Measured (us) as few / many:
-// 16 requests' single tokens with 2048 - 8192 cached 6.0 / 7.7, 4 x 8192 tokens 329 / 238
-// (1.37 GB: 85% of the measured copy bandwidth).
+// three blocks an SM. Others need warps: five blocks an SM. Measured (us) as few / many:
+// 16 requests' single tokens with 2048 - 8192 cached 5.7 / 7.7, 4 x 8192 tokens 329 / 246
+// (1.37 GB: 82% of the measured copy bandwidth).
 template <bool kFew>
 struct Depth {
-  static constexpr int kBlocks = kFew ? 3 : 6;
+  static constexpr int kBlocks = kFew ? 3 : 5;
   static constexpr int kOld = kFew ? 8 : 4;     // cached rows
   static constexpr int kNew = kFew ? 2 : 1;     // tokens of new keys and values beside those at work
 };
@@ -63,7 +63,8 @@ struct RopeArgs {
   int H, H_q, ps_shift, num_blocks, bt_stride, batch, T, max_new, ret_cap, advanced;
   int max_pos, rot, axes, sec[4];          // sec: first pair of each axis's section
   float eps;
-  int k_units, pages, k_groups;            // K warps: requests x pages each can touch x groups of KV heads
+  int k_units, pages, k_groups;            // requests x pages each can touch x groups of KV heads
+  int page_warps;                          // warps that share a unit
   int q_chunk, q_chunks;                   // query heads per warp
 };
 
@@ -259,16 +260,26 @@ __device__ __forceinline__ uint32_t max2(uint32_t x, uint32_t y, __half) {
   return *reinterpret_cast<const uint32_t*>(&r);
 }
 
-// Running statistics of a lane's columns; minimum and maximum in the elements' own type.
+// Running statistics of a lane's columns; minimum and maximum in the elements' own type, the sum in float32 with the
+// exact errors of its additions summed beside it.
 template <typename T, int NP>
 struct Columns {
   uint32_t mn[NP], mx[NP];
-  float sum[2 * NP];
-  uint32_t inexact = 0;                      // bit i: a rounded addition in column i's sum
+  float sum[2 * NP], err[2 * NP];
+  uint32_t rounded = 0;                      // bit i: an addition of column i's sum has rounded
   __device__ __forceinline__ Columns() {
     const uint32_t inf = Elem<T>::pack(INFINITY, INFINITY);
 #pragma unroll
-    for (int i = 0; i < NP; ++i) mn[i] = inf, mx[i] = inf | 0x80008000u, sum[2 * i] = sum[2 * i + 1] = 0.f;
+    for (int i = 0; i < NP; ++i) mn[i] = inf, mx[i] = inf | 0x80008000u;
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) sum[i] = err[i] = 0.f;
+  }
+  __device__ __forceinline__ void add_to(int i, float x) {
+    const float t = sum[i] + x, y = t - sum[i];
+    const float e = (sum[i] - (t - y)) + (x - y);
+    sum[i] = t;
+    err[i] += e;
+    rounded |= uint32_t(e != 0.f) << i;
   }
   __device__ __forceinline__ void add(const Row<NP>& r) {
     float x[2 * NP];
@@ -279,29 +290,57 @@ struct Columns {
       mx[i] = max2(mx[i], r.w[i], T());
     }
 #pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) add_to(i, x[i]);
+  }
+  // To and from shared memory, a lane's words 32 apart.
+  static constexpr int kWords = 6 * NP + 1;
+  __device__ __forceinline__ void save(uint32_t* p) const {
+#pragma unroll
+    for (int i = 0; i < NP; ++i) p[32 * i] = mn[i], p[32 * (NP + i)] = mx[i];
+#pragma unroll
     for (int i = 0; i < 2 * NP; ++i) {
-      bool exact = true;
-      two_sum(sum[i], x[i], exact);
-      inexact |= uint32_t(!exact) << i;
+      p[32 * (2 * NP + i)] = __float_as_uint(sum[i]);
+      p[32 * (4 * NP + i)] = __float_as_uint(err[i]);
+    }
+    p[32 * 6 * NP] = rounded;
+  }
+  __device__ __forceinline__ void join(const uint32_t* p) {
+    rounded |= p[32 * 6 * NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      mn[i] = min2(mn[i], p[32 * i], T());
+      mx[i] = max2(mx[i], p[32 * (NP + i)], T());
+    }
+#pragma unroll
+    for (int i = 0; i < 2 * NP; ++i) {
+      add_to(i, __uint_as_float(p[32 * (2 * NP + i)]));
+      err[i] += __uint_as_float(p[32 * (4 * NP + i)]);
     }
   }
 };
 
-// Rare: the float64 mean of a column (half `hi` of words p, p + C, ..) of the pool.
+// The float64 mean of a column, rounded once, where its float32 sum has rounded: from the sum and its errors. The sum of
+// the n errors, each at most 2^-24 n |x|, is off by at most n 2^-24 of theirs, n^3 2^-48 |x| with |x| the column's
+// largest value; where the mean could round two ways within that (or is not finite), from the pool's rows
+// (half `hi` of words p, p + C, ..).
 template <typename T>
-__device__ __noinline__ uint16_t mean_f64(const uint32_t* p, int C, int fill, bool hi) {
+__device__ __noinline__ uint16_t mean_f64(float sum, float err, float big, const uint32_t* p, int C, int fill, bool hi) {
+  const double n = double(fill), mean = (double(sum) + double(err)) / n, off = n * n * 0x1p-48 * double(big);
+  const uint16_t lo = Elem<T>::from_f64(mean - off);
+  if (lo == Elem<T>::from_f64(mean + off) && fabsf(sum) < 0x1p126f) return lo;
   double d = 0.0;
   for (int s = 0; s < fill; ++s) {
     const uint32_t w = p[int64_t(s) * C];
     d += double(hi ? Elem<T>::hi(w) : Elem<T>::lo(w));
   }
-  return Elem<T>::from_f64(d / double(fill));
+  return Elem<T>::from_f64(d / n);
 }
 
 // Statistics of the lane's columns of (block, head), written; the page's rows are in the pool.
 template <typename T, int D, int NP>
 __device__ __forceinline__ void write_stats(const RopeArgs& a, const Columns<T, NP>& st, int64_t tile, int blk, int h,
                                             int ca, int cb, int fill) {
+  using E = Elem<T>;
   constexpr int C = D / 2;
   const uint32_t* kp = static_cast<const uint32_t*>(a.k) + tile * C;
   uint32_t* m = static_cast<uint32_t*>(a.meta) + (int64_t(blk) * a.H + h) * 3 * C;
@@ -311,11 +350,13 @@ __device__ __forceinline__ void write_stats(const RopeArgs& a, const Columns<T, 
     const int c0 = (half ? cb : ca) >> 1;    // first column pair
 #pragma unroll
     for (int i = 0; i < NP / 2; ++i) {
-      const int x = NP * half + 2 * i;
+      const int x = NP * half + 2 * i, w = NP / 2 * half + i;
       uint16_t m0 = 0, m1 = 0;
-      if (((st.inexact >> x) & 1u) || !mean_f32<T>(st.sum[x], fill, m0)) m0 = mean_f64<T>(kp + c0 + i, C, fill, false);
-      if (((st.inexact >> (x + 1)) & 1u) || !mean_f32<T>(st.sum[x + 1], fill, m1))
-        m1 = mean_f64<T>(kp + c0 + i, C, fill, true);
+      if (((st.rounded >> x) & 1u) || !mean_f32<T>(st.sum[x], fill, m0))
+        m0 = mean_f64<T>(st.sum[x], st.err[x], fmaxf(fabsf(E::lo(st.mn[w])), fabsf(E::lo(st.mx[w]))), kp + c0 + i, C, fill, false);
+      if (((st.rounded >> (x + 1)) & 1u) || !mean_f32<T>(st.sum[x + 1], fill, m1))
+        m1 = mean_f64<T>(st.sum[x + 1], st.err[x + 1], fmaxf(fabsf(E::hi(st.mn[w])), fabsf(E::hi(st.mx[w]))), kp + c0 + i, C,
+                         fill, true);
       mean[i] = uint32_t(m0) | (uint32_t(m1) << 16);
     }
     store_words<NP / 2>(m + c0, st.mn + NP / 2 * half);
@@ -327,24 +368,53 @@ __device__ __forceinline__ void write_stats(const RopeArgs& a, const Columns<T, 
   }
 }
 
-// Warp `u`: the new keys and values of a group of KV heads on one page.
+// The rows of unit `u` (a group of KV heads on one page) that warp `part` of the a.page_warps that share it has.
+template <int RPW>
+struct PageRows {
+  int h, b, start, blk, fill;          // head of this lane, request, first position of the page, its block and rows
+  int lo, s_old, s_new, hi;            // this warp's slots: [lo, s_old) cached before, [s_new, hi) new
+  int row0, pos0;                      // row of the call at slot 0; old length
+  bool on, live;                       // there is such a head; there is something to do
+  __device__ __forceinline__ PageRows(const RopeArgs& a, int u, int part, bool unit, int sub, bool report) {
+    live = unit;
+    if (!unit) u = 0;
+    h = (u % a.k_groups) * RPW + sub;
+    on = h < a.H;
+    const int rest = u / a.k_groups, i = rest % a.pages;
+    b = rest / a.pages;
+    const int c0 = a.new_cu[b], c1 = a.new_cu[b + 1], L = a.seq_lens[b];
+    int L_old = 0, n = 0;
+    live = live && plan(a, L, c0, c1, report && part == 0 && u % a.k_groups == 0 && i == 0, L_old, n);
+    const int ps = 1 << a.ps_shift, p = (L_old >> a.ps_shift) + i;
+    live = live && p <= ((L_old + n - 1) >> a.ps_shift);
+    start = p << a.ps_shift;
+    blk = live ? a.bt[int64_t(b) * a.bt_stride + p] : -1;
+    if (live && (blk < 0 || blk >= a.num_blocks)) {
+      if (report) flag(a.status, SA_DEV_BAD_BLOCK);
+      live = false;
+    }
+    pos0 = L_old;
+    row0 = c0 + start - L_old;
+    fill = min(ps, L_old + n - start);
+    const int first = max(0, L_old - start);
+    lo = part * (ps / a.page_warps);
+    hi = live ? min(fill, lo + ps / a.page_warps) : 0;
+    s_new = max(lo, first);
+    s_old = min(first, hi);
+  }
+};
+
+// The new keys and values of unit `u` and the statistics of its page. All warps of a block call it.
 template <typename T, int D, bool kInter, bool kFew>
-__device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
+__device__ __forceinline__ void key_unit(const RopeArgs& a, int u, int part, bool live, uint32_t* joint) {
   constexpr int NP = kKeyPairs, LPR = D / (2 * NP), RPW = 32 / LPR, kKeyBatch = Depth<kFew>::kNew, kOldBatch = Depth<kFew>::kOld;
   const int lane = threadIdx.x & 31, col = 2 * NP * (lane % LPR);
-  const int h = (u % a.k_groups) * RPW + lane / LPR;
-  const int rest = u / a.k_groups, b = rest / a.pages, i = rest % a.pages;
-  const int c0 = a.new_cu[b], c1 = a.new_cu[b + 1], L = a.seq_lens[b];
-  int L_old, n;
-  if (!plan(a, L, c0, c1, lane == 0 && u % a.k_groups == 0 && i == 0, L_old, n)) return;
-  const int ps = 1 << a.ps_shift;
-  const int p = (L_old >> a.ps_shift) + i;
-  if (p > ((L_old + n - 1) >> a.ps_shift)) return;
+  const PageRows<RPW> r(a, u, part, live, lane / LPR, lane == 0);
   const Lane<kInter, NP> ln(a, lane % LPR);
-  const bool on = h < a.H;
-  const int start = p << a.ps_shift;
-  const int s_new = max(0, L_old - start), fill = min(ps, L_old + n - start);
-  const int row0 = c0 + start - L_old;       // row of the call at slot 0
+  const int h = r.h, start = r.start, blk = r.blk, fill = r.fill, ps = 1 << a.ps_shift;
+  const int lo = r.lo, s_old = r.s_old, s_new = r.s_new, hi = r.hi, row0 = r.row0;
+  const bool on = r.on;
+  live = r.live;
   const uint16_t* kn = static_cast<const uint16_t*>(a.k_new) + h * D;
   const uint16_t* vn = static_cast<const uint16_t*>(a.v_new) + h * D + col;
   Row<NP> x[kKeyBatch], v[kKeyBatch];
@@ -356,7 +426,7 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
       const int s = s0 + j, t = row0 + s;
       if (a.positions && (s == s_new || (s & 31) == 0)) {
         const int mine = (s & ~31) + lane;
-        if (mine >= s_new && mine < fill) load_positions(a, row0 + mine, at);
+        if (mine >= s_new && mine < hi) load_positions(a, row0 + mine, at);
       }
       int pos[4] = {start + s, 0, 0, 0};
       if (a.positions) {
@@ -365,7 +435,7 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
           if (x < a.axes) pos[x] = __shfl_sync(kFull, at[x], s & 31);
       }
       x[j] = v[j] = Row<NP>{};
-      if (s < fill) {
+      if (s < hi) {
         if (on) {
           x[j] = ln.load(kn + t * a.k_stride);
           load_words<NP>(v[j].w, vn + t * a.v_stride);
@@ -374,55 +444,57 @@ __device__ __forceinline__ void key_unit(const RopeArgs& a, int u) {
       }
     }
   };
-  const int blk = a.bt[int64_t(b) * a.bt_stride + p];
   fetch(s_new);
-  if (blk < 0 || blk >= a.num_blocks) {
-    if (lane == 0) flag(a.status, SA_DEV_BAD_BLOCK);
-    return;
-  }
   const Row<NP> w = weights(ln, a.k_weight);
   const int64_t tile = (int64_t(blk) * a.H + h) * ps;
   uint16_t* kp = static_cast<uint16_t*>(a.k) + tile * D;
   uint16_t* vp = static_cast<uint16_t*>(a.v) + tile * D + col;
   Columns<T, NP> st;
   if (a.meta && on) {
-    for (int s0 = 0; s0 < s_new; s0 += kOldBatch) {
+    for (int s0 = lo; s0 < s_old; s0 += kOldBatch) {
       Row<NP> old[kOldBatch];
 #pragma unroll
       for (int j = 0; j < kOldBatch; ++j)
-        if (s0 + j < s_new) old[j] = ln.load(kp + (s0 + j) * D);
+        if (s0 + j < s_old) old[j] = ln.load(kp + (s0 + j) * D);
 #pragma unroll
       for (int j = 0; j < kOldBatch; ++j)
-        if (s0 + j < s_new) st.add(old[j]);
+        if (s0 + j < s_old) st.add(old[j]);
     }
   }
   __syncwarp();
-  for (int s0 = s_new; s0 < fill; s0 += kKeyBatch) {
+  for (int s0 = s_new; s0 < hi; s0 += kKeyBatch) {
     Row<NP> y[kKeyBatch], z[kKeyBatch];
 #pragma unroll
     for (int j = 0; j < kKeyBatch; ++j) {
       y[j] = transform<T, D, kInter, NP>(ln, x[j], g[j], a.k_weight != nullptr, w, a.eps);
       z[j] = v[j];
     }
-    if (s0 + kKeyBatch < fill) fetch(s0 + kKeyBatch);
+    if (s0 + kKeyBatch < hi) fetch(s0 + kKeyBatch);
 #pragma unroll
     for (int j = 0; j < kKeyBatch; ++j) {
       const int s = s0 + j;
-      if (s < fill && on) {
+      if (s < hi && on) {
         ln.store(kp + s * D, y[j]);
         store_words<NP>(vp + s * D, z[j].w);
         if (a.meta) st.add(y[j]);
       }
     }
   }
-  if (!on) return;
-  if (a.meta) write_stats<T, D, NP>(a, st, tile, blk, h, ln.ca, ln.cb, fill);
-  for (int s = s_new + lane % LPR; s < fill; s += LPR) {
+  if (a.page_warps > 1 && a.meta) {          // the page's statistics meet in its first warp
+    uint32_t* mine = joint + (threadIdx.x >> 5) * 32 * Columns<T, NP>::kWords + lane;
+    if (part > 0) st.save(mine);
+    __syncthreads();
+    if (part == 0)
+      for (int q = 1; q < a.page_warps; ++q) st.join(mine + q * 32 * Columns<T, NP>::kWords);
+  }
+  if (!on || !live) return;
+  if (a.meta && part == 0) write_stats<T, D, NP>(a, st, tile, blk, h, ln.ca, ln.cb, fill);
+  for (int s = s_new + lane % LPR; s < hi; s += LPR) {
     if (a.hh) a.hh[(int64_t(blk) * ps + s) * a.H + h] = 0;
     if (a.ret_pos) {
-      const int cpos = a.ret_cnt[b * a.H + h] + (start + s - L_old);
+      const int cpos = a.ret_cnt[r.b * a.H + h] + (start + s - r.pos0);
       if (cpos < 0 || cpos >= a.ret_cap) flag(a.status, SA_DEV_OVERFLOW);
-      else a.ret_pos[(int64_t(b) * a.H + h) * a.ret_cap + cpos] = start + s;
+      else a.ret_pos[(int64_t(r.b) * a.H + h) * a.ret_cap + cpos] = start + s;
     }
   }
 }
@@ -485,11 +557,12 @@ __device__ __forceinline__ void query_unit(const RopeArgs& a, int u) {
 
 template <typename T, int D, bool kInter, bool kFew>
 __global__ void __launch_bounds__(kThreads, Depth<kFew>::kBlocks) rope_append_kernel(const __grid_constant__ RopeArgs a) {
-  const int k_blocks = (a.k_units + kWarps - 1) / kWarps;
+  extern __shared__ uint32_t joint[];        // a block's column statistics, where warps share pages
+  const int per_block = kWarps / a.page_warps, k_blocks = (a.k_units + per_block - 1) / per_block;
   const int warp = threadIdx.x >> 5;
   if (int(blockIdx.x) < k_blocks) {
-    const int u = blockIdx.x * kWarps + warp;
-    if (u < a.k_units) key_unit<T, D, kInter, kFew>(a, u);
+    const int u = blockIdx.x * per_block + warp / a.page_warps;
+    key_unit<T, D, kInter, kFew>(a, u, warp % a.page_warps, u < a.k_units, joint);
   } else {
     const int u = (blockIdx.x - k_blocks) * kWarps + warp;
     if (u < a.T * a.q_chunks) query_unit<T, D, kInter>(a, u);
@@ -510,10 +583,11 @@ __global__ void rope_advance_kernel(const __grid_constant__ RopeArgs a) {
 
 template <typename T, int D>
 cudaError_t launch(const RopeArgs& a, unsigned blocks, bool inter, cudaStream_t s) {
+  const size_t smem = a.page_warps > 1 ? sizeof(uint32_t) * kWarps * 32 * Columns<T, kKeyPairs>::kWords : 0;
   const bool few = blocks <= unsigned(Depth<true>::kBlocks * sm_count());
   auto k = few ? (inter ? rope_append_kernel<T, D, true, true> : rope_append_kernel<T, D, false, true>)
                : (inter ? rope_append_kernel<T, D, true, false> : rope_append_kernel<T, D, false, false>);
-  return launch_ex(k, dim3(blocks), dim3(kThreads), 0, s, false, 1, a);
+  return launch_ex(k, dim3(blocks), dim3(kThreads), smem, s, false, 1, a);
 }
 
 bool bad_stride(int64_t stride, int64_t row) { return stride < row || stride % 8; }
@@ -579,9 +653,16 @@ extern "C" sa_status sa_append_kv_rope(const sa_cache* cache, const sa_batch* ba
     a.q_chunk *= 2;
   a.q_chunks = q ? (num_q_heads + a.q_chunk - 1) / a.q_chunk : 0;
   const int64_t q_units = int64_t(num_tokens) * a.q_chunks;
-  if (k_units > 0x7fffff00 || q_units > 0x7fffff00) return SA_ERR_UNSUPPORTED;
+  if (k_units > 0x1fffff00 || q_units > 0x7fffff00) return SA_ERR_UNSUPPORTED;
   a.k_units = int(k_units);
-  const unsigned blocks = unsigned((k_units + kWarps - 1) / kWarps + (q_units + kWarps - 1) / kWarps);
+  // warps that share a page's rows: as many as give each at least 8 of them, while the pages alone leave SMs waiting
+  // (us with 1 / 2 / 4 warps a page of 32 and 128 tokens: 56 / 27 / 21 and 207 / 182 / 91 for 3 k and 35 k tokens of
+  // 4 KV heads; 4 x 8192 tokens in pages of 16: 247 / 254)
+  a.page_warps = 1;
+  while (a.page_warps < kWarps && cache->page_size >= 16 * a.page_warps && k_units * a.page_warps < int64_t(24) * sm_count())
+    a.page_warps *= 2;
+  const int per_block = kWarps / a.page_warps;
+  const unsigned blocks = unsigned((k_units + per_block - 1) / per_block + (q_units + kWarps - 1) / kWarps);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SA_BF16, inter = rope->interleaved != 0;
   const cudaError_t e = D == 128 ? (bf ? launch<__nv_bfloat16, 128>(a, blocks, inter, s) : launch<__half, 128>(a, blocks, inter, s))
