@@ -29,7 +29,6 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kStages = 3;
 constexpr int kCtasPerSm = 2;
 constexpr int kMaxBatch = 1024;
 constexpr int kFlight = 8;                 // parts a merging thread has in flight
@@ -52,6 +51,8 @@ struct PagedDecodeArgs {
 
 template <int D>
 struct Tile {
+  // Tiles a warp has under way or at work. D = 128, 128 k tokens of 4 requests: 319 us with 3, 307 with 2.
+  static constexpr int kStages = D == 128 ? 2 : 3;
   static constexpr int kBytes = 16 * D * 2;
   static constexpr int kChunks = D / 8;
   static constexpr int kRowsPerOp = 32 / kChunks;
@@ -59,7 +60,7 @@ struct Tile {
   static constexpr int kStageBytes = 2 * kBytes;
   static constexpr int kRing = kWarps * kStages * kStageBytes;
   static constexpr int kMerge = 4 * (kWarps * 32 + kWarps * 16 * (D + 4));
-  static constexpr int kSmem = (kRing > kMerge ? kRing : kMerge) + 1024;
+  static constexpr int kSmem = kRing + kMerge + 1024;
 };
 
 template <typename T, int D, bool kTma>
@@ -69,6 +70,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   using E = Elem<T>;
   using TL = Tile<D>;
   extern __shared__ __align__(128) uint8_t smem_raw[];
+  constexpr int kStages = TL::kStages;
   __shared__ uint32_t s_mask[kWarps][kStages];
   __shared__ __align__(8) uint64_t s_bar[kWarps][kStages];
   __shared__ int s_last;
@@ -111,56 +113,24 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   int cnt = 0;                                  // tiles this warp has issued and consumed in all
   bool alive = true;
 
-  while (at < stop) {
-    // the request and head of group `at`
-    int b = 0, before = 0, mine = 0;
-    for (int b0 = 0; b0 < a.batch; b0 += 32) {
-      const int x = b0 ? groups_of(b0) : head_groups;
-      int sum = x;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int y = __shfl_up_sync(kFull, sum, o);
-        if (lane >= o) sum += y;
-      }
-      const int k = __popc(__ballot_sync(kFull, before + sum <= at));
-      if (k < 32) {
-        b = b0 + k;
-        mine = __shfl_sync(kFull, x, k);
-        before += __shfl_sync(kFull, sum, k) - mine;
-        break;
-      }
-      before += __shfl_sync(kFull, sum, 31);
-    }
-    const int groups = mine / a.H_kv;
-    const int h = (at - before) / groups, unit_at = before + h * groups;
-    const int gi = at - unit_at, ge = min(groups, gi + stop - at);
-    at += ge - gi;
-    const int L = length(b), Lc = min(L, cap);
-    const Span<16> sp = span(L);
-    const int w0 = a.window > 0 ? max(0, L - a.window) : 0;
-    const int t_begin = gi * 4, t_end = min(ge * 4, sp.tiles);
-    const int nt = t_begin + warp < t_end ? (t_end - t_begin - warp + kWarps - 1) / kWarps : 0;
-    const int32_t* btb = a.bt + int64_t(b) * a.bt_stride;
+  // The part of a unit at work: request b, KV head h, groups [gi, ge) of its `groups` (the first is group unit_at of
+  // all), the lengths and the visible range, this warp's nt tiles from t_begin + warp on, every kWarps-th.
+  int b = 0, h = 0, gi = 0, ge = 0, groups = 1, unit_at = 0, Lc = 0, w0 = 0, t_begin = 0, nt = 0;
+  Span<16> sp(-1, -1, 0, 0, 0);
+  const int32_t* btb = a.bt;
+  uint32_t qa[D / 16][4];                       // Q as the A operand (rows: the query heads, zero beyond G)
+  float o[D / 8][4], m_r[2], l_r[2];
+  // Block ids are loaded a batch of tiles ahead, one id a lane: a tile has one page, or 16 / page_size of them.
+  const int ids_shift = max(0, 4 - pss);                 // log2 of the ids of a tile
+  const int per_batch = 32 >> ids_shift;
+  int ids = -1, ids_next = -1;
+  bool running = false;
 
-    // Q as the A operand (rows: the query heads of this KV head, zero beyond G)
-    uint32_t qa[D / 16][4];
-    {
-      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) +
-                                                             (int64_t(b) * a.H_q + int64_t(h) * G) * D);
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        const int c0 = (kk * 16 + 2 * tq) >> 1, c1 = c0 + 4;
-        qa[kk][0] = g < G ? qp[g * (D / 2) + c0] : 0u;
-        qa[kk][1] = g + 8 < G ? qp[(g + 8) * (D / 2) + c0] : 0u;
-        qa[kk][2] = g < G ? qp[g * (D / 2) + c1] : 0u;
-        qa[kk][3] = g + 8 < G ? qp[(g + 8) * (D / 2) + c1] : 0u;
-      }
-    }
-
-    // Block ids are loaded a batch of tiles ahead, one id a lane: a tile has one
-    // page, or 16 / page_size of them.
-    const int ids_shift = max(0, 4 - pss);               // log2 of the ids of a tile
-    const int per_batch = 32 >> ids_shift;
+  while (true) {
+    // what the merge of the part just done needs; then the next part begins, so that its first tiles are under way
+    // during the merge
+    const int d_b = b, d_h = h, d_gi = gi, d_ge = ge, d_groups = groups, d_unit_at = unit_at;
+    const bool more = at < stop;
     auto load_ids = [&](int i) {
       const int ti = i + (lane >> ids_shift);
       int id = -1;
@@ -176,8 +146,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
       return id;
     };
-    int ids = -1, ids_next = load_ids(0);
-
     auto issue = [&](int i) {
       if ((i & (per_batch - 1)) == 0) {
         ids = ids_next;
@@ -227,15 +195,204 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       }
     };
 
-    float o[D / 8][4];
+    if (more) {
+      // the request and head of group `at`
+      int before = 0, mine = 0;
+      for (int b0 = 0; b0 < a.batch; b0 += 32) {
+        const int x = b0 ? groups_of(b0) : head_groups;
+        int sum = x;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(kFull, sum, o);
+          if (lane >= o) sum += y;
+        }
+        const int k = __popc(__ballot_sync(kFull, before + sum <= at));
+        if (k < 32) {
+          b = b0 + k;
+          mine = __shfl_sync(kFull, x, k);
+          before += __shfl_sync(kFull, sum, k) - mine;
+          break;
+        }
+        before += __shfl_sync(kFull, sum, 31);
+      }
+      groups = mine / a.H_kv;
+      h = (at - before) / groups, unit_at = before + h * groups;
+      gi = at - unit_at, ge = min(groups, gi + stop - at);
+      at += ge - gi;
+      const int L = length(b);
+      Lc = min(L, cap);
+      sp = span(L);
+      w0 = a.window > 0 ? max(0, L - a.window) : 0;
+      t_begin = gi * 4;
+      const int t_end = min(ge * 4, sp.tiles);
+      nt = t_begin + warp < t_end ? (t_end - t_begin - warp + kWarps - 1) / kWarps : 0;
+      btb = a.bt + int64_t(b) * a.bt_stride;
+      ids_next = load_ids(0);
+      const uint32_t* qp = reinterpret_cast<const uint32_t*>(static_cast<const T*>(a.q) +
+                                                             (int64_t(b) * a.H_q + int64_t(h) * G) * D);
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        const int c0 = (kk * 16 + 2 * tq) >> 1, c1 = c0 + 4;
+        qa[kk][0] = g < G ? qp[g * (D / 2) + c0] : 0u;
+        qa[kk][1] = g + 8 < G ? qp[(g + 8) * (D / 2) + c0] : 0u;
+        qa[kk][2] = g < G ? qp[g * (D / 2) + c1] : 0u;
+        qa[kk][3] = g + 8 < G ? qp[(g + 8) * (D / 2) + c1] : 0u;
+      }
+#pragma unroll
+      for (int i = 0; i < kStages - 1; ++i) {
+        if (i < nt && alive) issue(i);
+        if constexpr (!kTma) cp_async_commit();
+      }
+    }
+    if (running) {
+#pragma unroll
+    for (int r = 0; r < 2; ++r) {
+      l_r[r] += __shfl_xor_sync(kFull, l_r[r], 1);
+      l_r[r] += __shfl_xor_sync(kFull, l_r[r], 2);
+    }
+
+    // merge the 4 warps in shared memory
+    constexpr int WS = D + 4;
+    float* wm = reinterpret_cast<float*>(smem + TL::kRing);
+    float* wl = wm + kWarps * 16;
+    float* wo = wl + kWarps * 16;
+    if (tq == 0) {
+      wm[warp * 16 + g] = m_r[0];
+      wm[warp * 16 + g + 8] = m_r[1];
+      wl[warp * 16 + g] = l_r[0];
+      wl[warp * 16 + g + 8] = l_r[1];
+    }
+#pragma unroll
+    for (int x = 0; x < D / 8; ++x) {
+      const int d = x * 8 + 2 * tq;
+      if (g < G) *reinterpret_cast<float2*>(&wo[(warp * G + g) * WS + d]) = make_float2(o[x][0], o[x][1]);
+      if (g + 8 < G) *reinterpret_cast<float2*>(&wo[(warp * G + g + 8) * WS + d]) = make_float2(o[x][2], o[x][3]);
+    }
+    __syncthreads();
+    if (threadIdx.x < G) {
+      const int row = threadIdx.x;
+      float M = -INFINITY, f[kWarps], tot = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * 16 + row]);
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float mw = wm[w * 16 + row];
+        f[w] = mw == -INFINITY ? 0.f : ex2_approx(mw - M);
+        tot = fmaf(wl[w * 16 + row], f[w], tot);
+      }
+      const float inv = tot > 0.f ? 1.0f / tot : 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) s_sf[w][row] = f[w] * inv;
+      s_rl[row] = tot > 0.f ? (M + lg2_approx(tot)) * kLn2 : -INFINITY;
+    }
+    __syncthreads();
+    auto merged = [&](int row, int d) {
+      float acc = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float sf = s_sf[w][row];
+        if (sf != 0.f) acc = fmaf(wo[(w * G + row) * WS + d], sf, acc);
+      }
+      return acc;
+    };
+    const int64_t row0 = int64_t(d_b) * a.H_q + int64_t(d_h) * G;
+    uint16_t* outp = static_cast<uint16_t*>(a.out) + row0 * D;
+    if (d_gi == 0 && d_ge == d_groups) {                       // the whole unit
+      for (int idx = threadIdx.x; idx < G * D; idx += kThreads) outp[idx] = E::from_f(merged(idx / D, idx % D));
+      if (a.lse && threadIdx.x < G) a.lse[row0 + threadIdx.x] = s_rl[threadIdx.x];
+    } else {
+      const int64_t slot = 2 * int64_t(blockIdx.x) + (d_gi == 0 ? 1 : 0);
+      for (int idx = threadIdx.x; idx < G * D; idx += kThreads)
+        a.part_o[slot * G * D + idx] = merged(idx / D, idx % D);
+      if (threadIdx.x < G) a.part_lse[slot * G + threadIdx.x] = s_rl[threadIdx.x];
+      // CTAs that hold parts of the unit: owners of its first to its last group
+      const int c_first = int(((int64_t(d_unit_at) + 1) * N - 1) / total);
+      const int c_last = int(((int64_t(d_unit_at) + d_groups) * N - 1) / total);
+      const int parts = c_last - c_first + 1;
+      __syncthreads();
+      const int unit = d_b * a.H_kv + d_h;
+      if (threadIdx.x == 0) s_last = ticket(&a.tickets[unit]) == parts - 1;
+      __syncthreads();
+      if (s_last) {
+        // A thread merges four columns of a row, kFlight parts in flight, in the order of the parts; where the rows
+        // leave threads over, `ways` of them take every ways-th batch of a column and meet in shared memory.
+        auto slot_of = [&](int p) { return 2 * int64_t(c_first + p) + (p == 0 ? 1 : 0); };
+        const int quads = G * (D / 4), ways = quads >= kThreads ? 1 : kThreads / quads;
+        float* meet = wo;                                    // [ways][quads][6]
+        for (int i = threadIdx.x; i < quads * ways; i += kThreads) {
+          const int quad = i % quads, way = i / quads, idx = 4 * quad, row = idx / D;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          float M = -INFINITY, tot = 0.f;
+          for (int p0 = way * kFlight; p0 < parts; p0 += ways * kFlight) {
+            float4 x[kFlight];
+            float z[kFlight];
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              z[k] = -INFINITY;
+              if (p0 + k < parts) {
+                const int64_t r = slot_of(p0 + k) * G;
+                z[k] = __ldcg(a.part_lse + r + row);
+                x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + r * D + idx));
+              }
+            }
+            float m = M;
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) m = fmaxf(m, z[k]);
+            const float f = M == -INFINITY ? 0.f : ex2_approx((M - m) * kLog2e);
+            tot *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
+            M = m;
+#pragma unroll
+            for (int k = 0; k < kFlight; ++k) {
+              if (z[k] == -INFINITY) continue;             // an empty part
+              const float w = ex2_approx((z[k] - M) * kLog2e);
+              tot += w;
+              acc.x = fmaf(w, x[k].x, acc.x);
+              acc.y = fmaf(w, x[k].y, acc.y);
+              acc.z = fmaf(w, x[k].z, acc.z);
+              acc.w = fmaf(w, x[k].w, acc.w);
+            }
+          }
+          if (ways > 1) {
+            float* mine = meet + int64_t(i) * 6;
+            mine[0] = M, mine[1] = tot, mine[2] = acc.x, mine[3] = acc.y, mine[4] = acc.z, mine[5] = acc.w;
+            continue;
+          }
+          const float f = tot > 0.f ? 1.0f / tot : 0.f;
+          *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
+          if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+        }
+        if (ways > 1) {
+          __syncthreads();
+          if (int(threadIdx.x) < quads) {
+            const int idx = 4 * threadIdx.x, row = idx / D;
+            float M = -INFINITY, tot = 0.f;
+            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int q = 0; q < ways; ++q) M = fmaxf(M, meet[(q * quads + threadIdx.x) * 6]);
+            for (int q = 0; q < ways; ++q) {
+              const float* x = meet + (q * quads + threadIdx.x) * 6;
+              const float w = x[0] == -INFINITY ? 0.f : ex2_approx((x[0] - M) * kLog2e);
+              tot = fmaf(w, x[1], tot);
+              acc.x = fmaf(w, x[2], acc.x);
+              acc.y = fmaf(w, x[3], acc.y);
+              acc.z = fmaf(w, x[4], acc.z);
+              acc.w = fmaf(w, x[5], acc.w);
+            }
+            const float f = tot > 0.f ? 1.0f / tot : 0.f;
+            *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
+            if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+          }
+        }
+        if (threadIdx.x == 0) a.tickets[unit] = 0;
+      }
+    }
+    __syncthreads();                                     // the merge area is free again
+    }
+    if (!more) break;
+    running = true;
 #pragma unroll
     for (int x = 0; x < D / 8; ++x) o[x][0] = o[x][1] = o[x][2] = o[x][3] = 0.f;
-    float m_r[2] = {-INFINITY, -INFINITY}, l_r[2] = {0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-      if (i < nt && alive) issue(i);
-      if constexpr (!kTma) cp_async_commit();
-    }
+    m_r[0] = m_r[1] = -INFINITY;
+    l_r[0] = l_r[1] = 0.f;
     for (int i = 0; i < nt && alive; ++i) {
       __syncwarp();
       if (i + kStages - 1 < nt) issue(i + kStages - 1);
@@ -327,157 +484,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         E::mma(o[2 * nd + 1], pa, r[2], r[3]);
       }
     }
-    if constexpr (!kTma) cp_async_wait<0>();
     if (kTma && !alive) {
       // leave no copy in flight (each wait is bounded)
       for (int i = 0; i < nt && lane == 0; ++i)
         if (!mbar_wait(smem_u32(&s_bar[warp][(cnt + i) % kStages]), ((cnt + i) / kStages) & 1, a.status)) break;
     }
     cnt += nt;
-#pragma unroll
-    for (int r = 0; r < 2; ++r) {
-      l_r[r] += __shfl_xor_sync(kFull, l_r[r], 1);
-      l_r[r] += __shfl_xor_sync(kFull, l_r[r], 2);
-    }
-    __syncthreads();
-
-    // merge the 4 warps in shared memory, over the ring
-    constexpr int WS = D + 4;
-    float* wm = reinterpret_cast<float*>(smem);
-    float* wl = wm + kWarps * 16;
-    float* wo = wl + kWarps * 16;
-    if (tq == 0) {
-      wm[warp * 16 + g] = m_r[0];
-      wm[warp * 16 + g + 8] = m_r[1];
-      wl[warp * 16 + g] = l_r[0];
-      wl[warp * 16 + g + 8] = l_r[1];
-    }
-#pragma unroll
-    for (int x = 0; x < D / 8; ++x) {
-      const int d = x * 8 + 2 * tq;
-      if (g < G) *reinterpret_cast<float2*>(&wo[(warp * G + g) * WS + d]) = make_float2(o[x][0], o[x][1]);
-      if (g + 8 < G) *reinterpret_cast<float2*>(&wo[(warp * G + g + 8) * WS + d]) = make_float2(o[x][2], o[x][3]);
-    }
-    __syncthreads();
-    if (threadIdx.x < G) {
-      const int row = threadIdx.x;
-      float M = -INFINITY, f[kWarps], tot = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) M = fmaxf(M, wm[w * 16 + row]);
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float mw = wm[w * 16 + row];
-        f[w] = mw == -INFINITY ? 0.f : ex2_approx(mw - M);
-        tot = fmaf(wl[w * 16 + row], f[w], tot);
-      }
-      const float inv = tot > 0.f ? 1.0f / tot : 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) s_sf[w][row] = f[w] * inv;
-      s_rl[row] = tot > 0.f ? (M + lg2_approx(tot)) * kLn2 : -INFINITY;
-    }
-    __syncthreads();
-    auto merged = [&](int row, int d) {
-      float acc = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        const float sf = s_sf[w][row];
-        if (sf != 0.f) acc = fmaf(wo[(w * G + row) * WS + d], sf, acc);
-      }
-      return acc;
-    };
-    const int64_t row0 = int64_t(b) * a.H_q + int64_t(h) * G;
-    uint16_t* outp = static_cast<uint16_t*>(a.out) + row0 * D;
-    if (gi == 0 && ge == groups) {                       // the whole unit
-      for (int idx = threadIdx.x; idx < G * D; idx += kThreads) outp[idx] = E::from_f(merged(idx / D, idx % D));
-      if (a.lse && threadIdx.x < G) a.lse[row0 + threadIdx.x] = s_rl[threadIdx.x];
-    } else {
-      const int64_t slot = 2 * int64_t(blockIdx.x) + (gi == 0 ? 1 : 0);
-      for (int idx = threadIdx.x; idx < G * D; idx += kThreads)
-        a.part_o[slot * G * D + idx] = merged(idx / D, idx % D);
-      if (threadIdx.x < G) a.part_lse[slot * G + threadIdx.x] = s_rl[threadIdx.x];
-      // CTAs that hold parts of the unit: owners of its first to its last group
-      const int c_first = int(((int64_t(unit_at) + 1) * N - 1) / total);
-      const int c_last = int(((int64_t(unit_at) + groups) * N - 1) / total);
-      const int parts = c_last - c_first + 1;
-      __syncthreads();
-      const int unit = b * a.H_kv + h;
-      if (threadIdx.x == 0) s_last = ticket(&a.tickets[unit]) == parts - 1;
-      __syncthreads();
-      if (s_last) {
-        // A thread merges four columns of a row, kFlight parts in flight, in the order of the parts; where the rows
-        // leave threads over, `ways` of them take every ways-th batch of a column and meet in shared memory.
-        auto slot_of = [&](int p) { return 2 * int64_t(c_first + p) + (p == 0 ? 1 : 0); };
-        const int quads = G * (D / 4), ways = quads >= kThreads ? 1 : kThreads / quads;
-        float* meet = reinterpret_cast<float*>(smem);        // [ways][quads][6]
-        for (int i = threadIdx.x; i < quads * ways; i += kThreads) {
-          const int quad = i % quads, way = i / quads, idx = 4 * quad, row = idx / D;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          float M = -INFINITY, tot = 0.f;
-          for (int p0 = way * kFlight; p0 < parts; p0 += ways * kFlight) {
-            float4 x[kFlight];
-            float z[kFlight];
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-              z[k] = -INFINITY;
-              if (p0 + k < parts) {
-                const int64_t r = slot_of(p0 + k) * G;
-                z[k] = __ldcg(a.part_lse + r + row);
-                x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + r * D + idx));
-              }
-            }
-            float m = M;
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) m = fmaxf(m, z[k]);
-            const float f = M == -INFINITY ? 0.f : ex2_approx((M - m) * kLog2e);
-            tot *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-            M = m;
-#pragma unroll
-            for (int k = 0; k < kFlight; ++k) {
-              if (z[k] == -INFINITY) continue;             // an empty part
-              const float w = ex2_approx((z[k] - M) * kLog2e);
-              tot += w;
-              acc.x = fmaf(w, x[k].x, acc.x);
-              acc.y = fmaf(w, x[k].y, acc.y);
-              acc.z = fmaf(w, x[k].z, acc.z);
-              acc.w = fmaf(w, x[k].w, acc.w);
-            }
-          }
-          if (ways > 1) {
-            float* mine = meet + int64_t(i) * 6;
-            mine[0] = M, mine[1] = tot, mine[2] = acc.x, mine[3] = acc.y, mine[4] = acc.z, mine[5] = acc.w;
-            continue;
-          }
-          const float f = tot > 0.f ? 1.0f / tot : 0.f;
-          *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
-          if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
-        }
-        if (ways > 1) {
-          __syncthreads();
-          if (int(threadIdx.x) < quads) {
-            const int idx = 4 * threadIdx.x, row = idx / D;
-            float M = -INFINITY, tot = 0.f;
-            float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-            for (int q = 0; q < ways; ++q) M = fmaxf(M, meet[(q * quads + threadIdx.x) * 6]);
-            for (int q = 0; q < ways; ++q) {
-              const float* x = meet + (q * quads + threadIdx.x) * 6;
-              const float w = x[0] == -INFINITY ? 0.f : ex2_approx((x[0] - M) * kLog2e);
-              tot = fmaf(w, x[1], tot);
-              acc.x = fmaf(w, x[2], acc.x);
-              acc.y = fmaf(w, x[3], acc.y);
-              acc.z = fmaf(w, x[4], acc.z);
-              acc.w = fmaf(w, x[5], acc.w);
-            }
-            const float f = tot > 0.f ? 1.0f / tot : 0.f;
-            *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
-            if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
-          }
-        }
-        if (threadIdx.x == 0) a.tickets[unit] = 0;
-      }
-    }
-    fence_proxy_async_smem();                            // the ring is refilled by the TMA engine
-    __syncthreads();
   }
+  if constexpr (!kTma) cp_async_wait<0>();
 }
 
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
