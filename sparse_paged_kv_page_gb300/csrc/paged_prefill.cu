@@ -153,18 +153,28 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Wo
   // that gives no more parts than CTAs. At most 96 requests (three a lane).
   int c0[3], n[3], L[3], units[3], steps[3];
   int most = 1;
+  int64_t rows = 0;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
     const int b = 32 * i + lane;
     c0[i] = n[i] = L[i] = units[i] = steps[i] = 0;
     if (b < a.batch) {
       c0[i] = a.new_cu[b], n[i] = a.new_cu[b + 1] - c0[i], L[i] = a.seq_lens[b];
-      if (n[i] > 0) {
+      if (c0[i] < 0 || int64_t(c0[i]) + n[i] > a.T) {
+        if (blockIdx.x == 0) flag(a.status, SA_DEV_BAD_COUNT);
+      } else if (n[i] > 0) {
+        rows += n[i];
         units[i] = (n[i] + per - 1) / per * a.H_kv;
         steps[i] = request_steps(a, L[i], n[i], per, cap);
       }
     }
     most = max(most, steps[i]);
+  }
+#pragma unroll
+  for (int o = 16; o; o >>= 1) rows += __shfl_xor_sync(kFull, rows, o);
+  if (rows > a.T) {                          // not a list of offsets within the rows: some part might have no CTA
+    if (blockIdx.x == 0 && lane == 0) flag(a.status, SA_DEV_BAD_COUNT);
+    return false;
   }
   most = __reduce_max_sync(kFull, most);
   int lo = kMinPart, hi = max(kMinPart, most);

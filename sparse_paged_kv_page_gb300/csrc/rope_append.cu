@@ -321,11 +321,12 @@ struct Columns {
 
 // The float64 mean of a column, rounded once, where its float32 sum has rounded: from the sum and its errors. The sum of
 // the n errors, each at most 2^-24 n |x|, is off by at most n 2^-24 of theirs, n^3 2^-48 |x| with |x| the column's
-// largest value; where the mean could round two ways within that (or is not finite), from the pool's rows
+// largest value (and float64 by 2^-50 of the mean); where it could round two ways within that (or is not finite), from
+// the pool's rows
 // (half `hi` of words p, p + C, ..).
 template <typename T>
 __device__ __noinline__ uint16_t mean_f64(float sum, float err, float big, const uint32_t* p, int C, int fill, bool hi) {
-  const double n = double(fill), mean = (double(sum) + double(err)) / n, off = n * n * 0x1p-48 * double(big);
+  const double n = double(fill), mean = (double(sum) + double(err)) / n, off = n * n * 0x1p-48 * double(big) + 0x1p-50 * fabs(mean);
   const uint16_t lo = Elem<T>::from_f64(mean - off);
   if (lo == Elem<T>::from_f64(mean + off) && fabsf(sum) < 0x1p126f) return lo;
   double d = 0.0;

@@ -102,11 +102,12 @@ def test_prompt_in_chunks_then_tokens(kw):
     _check_cache(dec, w, keys, values)
 
 
-def test_rotated_sparse_steps_equal_steps_on_turned_inputs():
+@pytest.mark.parametrize("ps", [16, 64, 128])
+def test_rotated_sparse_steps_equal_steps_on_turned_inputs(ps):
     """The sparse chain with a rotation is the chain without one on the turned queries and keys, bit for bit."""
     from sparse_paged_kv_page_gb300.step import SparseDecoder
-    dec, w, rand = _decoder(2, topk=4)
-    plain = SparseDecoder(batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=16,
+    dec, w, rand = _decoder(2, topk=4, ps=ps)
+    plain = SparseDecoder(batch=2, num_q_heads=8, num_kv_heads=2, head_dim=128, page_size=ps,
                           num_blocks=dec.cache.k.shape[0], bt_stride=dec.bt_stride, topk=4)
     plain.set_block_table(dec.block_table)
     lens = [200, 77]
@@ -121,7 +122,7 @@ def test_rotated_sparse_steps_equal_steps_on_turned_inputs():
         want = plain.step(dec.q_rot, new, vn)
         assert torch.equal(out, want) and torch.equal(dec.sel_idx, plain.sel_idx) and torch.equal(dec.lse, plain.lse)
     for b in range(2):
-        n = -(-(lens[b] + 4) // 16)
+        n = -(-(lens[b] + 4) // ps)
         blk = dec.block_table[b, :n].long()
         assert torch.equal(dec.cache.meta[blk], plain.cache.meta[blk])
 

@@ -362,3 +362,13 @@ def test_prefill_bad_data_is_flagged():
     want = attention64(q[6:8], *(x[:2] for x in p.seqs[1]), torch.arange(2, device="cuda"), 128 ** -0.5, 0, 0)
     check_attention(out[6:8], None, want)
     assert bool((out[8:] == 3.0).all())
+    # overlapping requests: nothing is written, and the workspace serves the next call
+    p = Problem([400, 300, 200], Hkv=1, G=2)
+    ws = p.S.alloc_paged_prefill_workspace(3, 1, 2, 128, 12)
+    q = p.rand(12, 2, 128)
+    out = torch.full_like(q, 3.0)
+    p.S.sa_paged_prefill(p.cache, p.batch, q, 2, torch.tensor([0, 12, 0, 12], dtype=torch.int32).cuda(), 0.0, out,
+                         workspace=ws, dev_status=p.status)
+    assert int(p.status) == 4 and bool((out == 3.0).all())
+    p.status.zero_()
+    _prefill(p, [4, 4, 4], ws=ws, q=q)
