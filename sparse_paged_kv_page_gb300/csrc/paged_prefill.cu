@@ -6,23 +6,27 @@
 // O and l are rescaled only where the weights 2^(scale (s - m)) have grown large; the
 // quotient o / l at the end makes any m right.
 //
-// A CTA owns 2 x 128 packed rows (token, query head of one KV head's group), so a
-// key is read once for all G heads, and walks the visible keys 128 at a time. The
-// products run on the 5th-generation tensor cores, accumulators in TMEM: S = Q K^T
-// (128 x 128, one per half), P over S's columns as the A operand from TMEM, O += P V.
-// A warpgroup takes each half, one row a thread (no shuffles): while one turns S into
-// P the tensor cores work for the other, so the time from S to P counts. One warp
-// issues the products, one the copies: keys and values in a ring of 128-row slots, page by page
-// through a tensor map (pages of 8 tokens and more), or row by row with cp.async
-// (smaller pages). Where the rows fill one half only, the halves take every other
-// step of the same rows and meet at the end.
+// A CTA owns 128 packed rows (token, query head of one KV head's group) at head dim 64,
+// two CTAs an SM, and 2 x 128 at 128, one an SM, so a key is read once for all G heads,
+// and walks the visible keys 128 at a time. The products run on the 5th-generation
+// tensor cores, accumulators in TMEM: S = Q K^T (128 x 128), P over S's columns as the A
+// operand from TMEM, O += P V. A warpgroup takes each 128 rows, one a thread (no
+// shuffles): while one turns S into P the tensor cores work for the other, so the time
+// from S to P counts. One warp issues the products, one the copies: keys and values in a
+// ring of 128-row slots, page by page through a tensor map (pages of 8 tokens and more),
+// or row by row with cp.async (smaller pages). Where the rows of a CTA of two halves
+// fill one only, the halves take every other step of the same rows and meet at the end.
 //
 // Value rows that no query of the CTA sees are zeroed in shared memory (a weight 0
 // times what a freed page holds must be 0), key rows masked.
 //
-// Bound by the tensor cores for prompts; for a few rows over a long cache by HBM,
-// where each item's keys are cut into parts of about the same number of steps, one
-// a CTA, and the last of an item's CTAs merges the parts in order.
+// Bound by the tensor cores for prompts (16384 tokens, 32 / 8 heads of 128, pages of 16:
+// 1310 us, 1.68 PFLOP/s, the power limit's rate for a dense product); at head dim 64 by
+// the rows' turn from S to P and the number of page copies (an operation costs about 80
+// cycles whatever its size: a prompt of 8192 over 4096 in pages of 16 1145 us, of 128
+// 920); for a few rows over a long cache by HBM, where each item's keys are cut into
+// parts of about the same number of steps, one a CTA, and the last of an item's CTAs
+// merges the parts in order.
 #include <type_traits>
 
 #include "common.cuh"
@@ -35,20 +39,15 @@ namespace sa {
 namespace {
 
 constexpr int kKeys = 128;                // positions per step
-constexpr int kMmaWarp = 8;               // warps 0-3 and 4-7: the softmax of the two halves
-constexpr int kSoftmaxThreads = 32 * kMmaWarp;
-constexpr int kThreads = kSoftmaxThreads + 128;
-// Registers: 384 threads are launched with 168 each; the softmax warpgroups take
-// 208 (a row of 128 scores a thread) of what the third one gives back:
-// 256 x 208 + 128 x 88 = 384 x 168.
-constexpr int kSoftmaxRegs = 208, kOtherRegs = 88;
 constexpr int kTileRing = 8;              // steps whose row masks are kept
 // The running maximum m follows the row only when a step's sum of weights 2^(scale (s - m)) passes this: below it
 // every weight is inside both 16-bit types, and float32 sums do not mind. So no step but the first looks for its
 // maximum (60 instructions of 380 a row), the sum that is made anyway tells.
 constexpr float kMostSum = 8192.0f;
 constexpr int kRun = 8;                   // words of P stored at a time
-constexpr int kMinPart = 4;               // steps of a part at least (a part costs about two)
+// Steps of a part at least, and of an item that is cut at all: a merge costs about six. Measured (us): 30 tokens x 64
+// heads over 500, 5 steps, whole 15 and in parts 22; over 2000, 16 steps, parts of 4 24 and of 6 28.
+constexpr int kMinPart = 4, kMinCut = 9;
 constexpr int kLag = 2;                   // row-by-row copies under way behind the newest
 
 struct PagedPrefillArgs {
@@ -59,27 +58,38 @@ struct PagedPrefillArgs {
   const int32_t* new_cu;
   void* out;
   float* lse;
-  float* part_o;        // [CTAs][256][D]
-  float* part_lse;      // [CTAs][256]
+  float4* part_o;       // [CTAs][D / 4][rows]: a warp stores adjacent rows
+  float* part_lse;      // [CTAs][rows]
   int32_t* tickets;     // [units]
   int32_t* status;
   int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink, items, split;
   float scale_log2;
 };
 
+// Halves of 128 packed rows of a CTA, a warpgroup each. At head dim 64 one, and two CTAs an SM, of which one works while
+// the other begins or ends (us, two halves / one: sliding-window prompts 177 / 166, 6 tokens of 4 requests over 30000 75 / 51).
+constexpr int ways(int D) { return D == 128 ? 2 : 1; }
+
 template <int D, bool kTma>
 struct Cfg {
   static constexpr int kProducers = kTma ? 1 : 3;                  // copy warps
   static constexpr int kHalves = D / 64;                           // 64-column halves of a row
+  static constexpr int kWays = ways(D);
+  static constexpr int kRows = 128 * kWays, kMmaWarp = 4 * kWays;  // the warps before are the softmax
+  static constexpr int kSoftmaxThreads = 32 * kMmaWarp, kThreads = kSoftmaxThreads + 128;
+  // Registers: the softmax warpgroups take (a row of 128 scores a thread) what the last one gives back:
+  // 256 x 208 + 128 x 88 = 384 x 168, 128 x 192 + 128 x 64 = 256 x 128.
+  static constexpr int kSoftmaxRegs = kWays == 2 ? 208 : 192, kOtherRegs = kWays == 2 ? 88 : 64;
   static constexpr int kGroupBytes = kHalves * 1024;               // 8 rows of a slot: [half][8 rows of 128 bytes]
   static constexpr int kSlotBytes = kKeys / 8 * kGroupBytes;
-  static constexpr int kSlots = D == 128 ? 5 : 8;
-  static constexpr int kQBytes = 2 * kSlotBytes;
-  // TMEM columns: S of the halves, O of the halves, and at D = 64, where there is room, P apart from S, so that the
-  // next step's S is made while this one's P is (sliding-window prompts 189 -> 179 us); at D = 128 P overwrites S.
-  static constexpr bool kApart = D == 64;
-  static constexpr int kOCol = 256, kPCol = kApart ? 384 : 0;
-  static constexpr int kPStride = kApart ? 64 : 128;
+  static constexpr int kSlots = 5;
+  static constexpr int kQBytes = kWays * kSlotBytes;
+  // TMEM columns: S of the halves, overwritten by P, and O of the halves. At D = 64, where there is room, S and P take turns
+  // in three blocks of 64 columns: step j has S in blocks j and j + 1 (mod 3) and P in block j, so that the next step's S,
+  // in the block left over and the one of the P before this (whose products come first), is made while P is (a prompt of
+  // 8192 over 4096, pages of 128: 945 -> 915 us against P in a place of its own, for which the products before had to end).
+  static constexpr bool kAhead = D == 64;
+  static constexpr int kOCol = kAhead ? 192 : 128 * kWays, kCols = 256 * kWays;
   static constexpr int kSharedAt = kQBytes + kSlots * kSlotBytes;
 };
 
@@ -89,8 +99,9 @@ struct Work {
 };
 
 struct Shared {
-  // of the halves: s made, s read (r), p made, products of a step complete (v; r and v where P is apart), the last ones (o)
-  uint64_t full[8], empty[8], q, s[2], r[2], p[2], v[2], o[2], edge, drain;
+  // of the halves: s made, p made, the last products complete (o); where S is made ahead p is of even and odd steps
+  // (the rows may be two P ahead of the products), s is read (r), a step's products complete (v)
+  uint64_t full[8], empty[8], q, s[2], p[2], o[2], r, v, edge, drain;
   uint32_t tile[kTileRing][1 + kKeys / 32];   // [0]: rows of the step are masked by the words that follow
   int64_t off[kKeys];                         // pool row of each position of a step copied row by row, -1: none
   float x[2][kKeys];                          // the second half's maxima and sums, where both have the same rows
@@ -140,9 +151,12 @@ __device__ __forceinline__ int request_steps(const PagedPrefillArgs& a, int L, i
   return Span<kKeys>(L - min(n, per), L - 1, min(max(L, 0), cap), a.window, a.n_sink).tiles;
 }
 
+// Parts of about `chunk` steps that an item is cut into.
+__device__ __forceinline__ int parts_of(int steps, int chunk) { return steps < kMinCut ? 1 : (steps + chunk - 1) / chunk; }
+
 // The CTA's work, found by one warp. False if there is none.
-__device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Work& w) {
-  const int lane = threadIdx.x & 31, per = 2 * (128 / a.G);
+__device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, int per, Work& w) {
+  const int lane = threadIdx.x & 31;
   if (!a.split) {
     // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
     w.h = blockIdx.x / a.items;
@@ -182,14 +196,14 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Wo
     const int mid = (lo + hi) >> 1;
     int parts = 0;
 #pragma unroll
-    for (int i = 0; i < 3; ++i) parts += units[i] * max(1, (steps[i] + mid - 1) / mid);
+    for (int i = 0; i < 3; ++i) parts += units[i] * parts_of(steps[i], mid);
     if (__reduce_add_sync(kFull, parts) <= int(gridDim.x)) hi = mid;
     else lo = mid + 1;
   }
   int before = 0, units_before = 0;
 #pragma unroll
   for (int i = 0; i < 3; ++i) {
-    const int np = max(1, (steps[i] + lo - 1) / lo), mine = units[i] * np;
+    const int np = parts_of(steps[i], lo), mine = units[i] * np;
     int x = mine, y = units[i];
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -215,7 +229,7 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, Wo
 }
 
 template <typename T, int D, bool kTma>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
     paged_prefill_kernel(const __grid_constant__ PagedPrefillArgs a, const __grid_constant__ CUtensorMap tmq,
                          const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv) {
   using E = Elem<T>;
@@ -225,12 +239,12 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint8_t* ring = smem + C::kQBytes;
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kSharedAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.G, pss = a.ps_shift, half_tokens = 128 / G;
+  const int G = a.G, pss = a.ps_shift, half_tokens = 128 / G, item_tokens = C::kWays * half_tokens;
   const int cap = int(min(int64_t(a.bt_stride) << pss, int64_t(0x7fffffff)));
 
   if (warp == 0) {
     Work w;
-    const bool any = find_work(a, cap, w);
+    const bool any = find_work(a, cap, item_tokens, w);
     if (any && w.item == 0 && w.h == 0 && w.part == 0 && lane == 0) {
       if (w.c0 < 0 || int64_t(w.c0) + w.n > a.T || w.L < w.n) flag(a.status, SA_DEV_BAD_COUNT);
       if (w.L > cap) flag(a.status, SA_DEV_OVERFLOW);
@@ -249,17 +263,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(smem_u32(&sh.q), 1);
     mbar_init(smem_u32(&sh.edge), 1);
     mbar_init(smem_u32(&sh.drain), 1);
+    mbar_init(smem_u32(&sh.r), 4);
+    mbar_init(smem_u32(&sh.v), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&sh.s[i]), 1);
       mbar_init(smem_u32(&sh.p[i]), 4);
       mbar_init(smem_u32(&sh.o[i]), 1);
-      mbar_init(smem_u32(&sh.r[i]), 4);
-      mbar_init(smem_u32(&sh.v[i]), 1);
     }
     mbar_init_fence();
-  } else if (warp == kMmaWarp) {
-    tc5_alloc(smem_u32(&sh.tmem), 512);
-  } else if (threadIdx.x == kSoftmaxThreads + 32) {
+  } else if (warp == C::kMmaWarp) {
+    tc5_alloc(smem_u32(&sh.tmem), C::kCols);
+  } else if (threadIdx.x == C::kSoftmaxThreads + 32) {
     prefetch_map(&tmq);
     if (kTma) {
       prefetch_map(&tmk);
@@ -272,24 +286,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tmem = sh.tmem;                                  // columns: S/P of the halves, then O of the halves
   const Work w = sh.work;
   if (w.b < 0) {
-    if (warp == kMmaWarp) tc5_dealloc(tmem, 512);
+    if (warp == C::kMmaWarp) tc5_dealloc(tmem, C::kCols);
     return;
   }
-  const int h = w.h, t0 = w.item * 2 * half_tokens, nt = min(2 * half_tokens, w.n - t0);
+  const int h = w.h, t0 = w.item * item_tokens, nt = min(item_tokens, w.n - t0);
   const int first = w.L - w.n + t0, last = first + nt - 1, len = min(max(w.L, 0), cap);
   const Span<kKeys> sp(first, last, len, a.window, a.n_sink);
   const int per = (sp.tiles + w.parts - 1) / w.parts;
   const int tb = min(sp.tiles, w.part * per), steps = min(sp.tiles, tb + per) - tb;
-  const bool two = nt > half_tokens;                              // the second half has rows of its own
-  const bool dual = !two && steps > 1;                            // the halves take every other step of the same rows
+  const bool two = C::kWays == 2 && nt > half_tokens;                              // the second half has rows of its own
+  const bool dual = C::kWays == 2 && !two && steps > 1;                            // the halves take every other step of the same rows
 
-  if (warp < kMmaWarp) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(kSoftmaxRegs));
+  if (warp < C::kMmaWarp) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(C::kSoftmaxRegs));
     // ------------------------------------------------------------- softmax: one row a thread
     const int half = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = uint32_t(warp & 3) << 21;              // TMEM lane 32 * (warp % 4)
     const uint32_t s_col = tmem + lanes + half * 128, o_col = tmem + lanes + C::kOCol + half * D;
-    const uint32_t p_col = tmem + lanes + C::kPCol + half * C::kPStride;
     const int t = (dual ? 0 : half * half_tokens) + row / G;
     const bool in = row / G < half_tokens && t < nt;
     const int pos = in ? first + t : -1;
@@ -298,6 +311,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool act = half == 0 || two || dual;
     const int stride = dual ? 2 : 1;
     uint32_t parity = 0;
+    int block = 0;                                                // first one of the step's S
     bool ok = steps > 0;
     // the warp's rows: steps that end behind `low`, or begin before `high`'s window, hide keys from one of them
     const int low = __reduce_min_sync(kFull, in ? min(pos, len - 1) : 0x7fffffff);
@@ -308,15 +322,18 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = wait_on(&sh.s[half], parity, sh, a.status) && ok;       // (a wait that gave up: the rest runs on to its end)
       __syncwarp();
       tc5_fence_after();
+      const uint32_t s_at = C::kAhead ? s_col + 64 * block : s_col, s_next = s_col + 64 * (block < 2 ? block + 1 : 0);
+      block = block < 2 ? block + 1 : 0;
       float s[kKeys];
 #pragma unroll
-      for (int c = 0; c < 4; ++c) tc5_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, s_col + 32 * c);
+      for (int c = 0; c < 4; ++c)
+        tc5_ld32(reinterpret_cast<uint32_t*>(s) + 32 * c, (C::kAhead && c >= 2 ? s_next - 64 : s_at) + 32 * c);
       const int bad = *reinterpret_cast<volatile int*>(&sh.bad);   // looked at with the sum below
       tc5_wait_ld();
-      if constexpr (C::kApart) {
+      if constexpr (C::kAhead) {
         tc5_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(smem_u32(&sh.r[half]));
+        if (lane == 0) mbar_arrive(smem_u32(&sh.r));
       }
       auto hide = [&]() {
         // columns seen: up to hi, from lo on or below sk, and those whose rows the step has
@@ -344,10 +361,35 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int x = 0; x < 4; ++x) mx[x] = fmaxf(mx[x], s[kKeys - 4 + x]);
         return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       };
-      // P = 2^(scale s - scale m) to TMEM, eight words at a time and one run behind; the row's sum
-      auto weights = [&](bool wait_p) {
+      if (cut || bad) hide();
+      float sum;
+      bool grow = j < stride;                                      // the reference follows the row's maximum
+#pragma unroll 1
+      for (int turn = 0;; ++turn) {
+        if (grow) {
+          const float m_new = in ? fmaxf(m, maximum()) : m;
+          if (j >= stride) {
+            // O and l follow; the products into O before this step are complete
+            if (C::kAhead) ok = wait_on(&sh.v, parity ^ 1, sh, a.status) && ok;
+            __syncwarp();
+            tc5_fence_after();
+            const float f = m_new == m ? 1.f : ex2_approx((m - m_new) * a.scale_log2);
+            l *= f;
+#pragma unroll
+            for (int c = 0; c < D / 16; ++c) {
+              float o[16];
+              tc5_ld16(reinterpret_cast<uint32_t*>(o), o_col + 16 * c);
+              tc5_wait_ld();
+#pragma unroll
+              for (int x = 0; x < 16; ++x) o[x] *= f;
+              tc5_st16(o_col + 16 * c, reinterpret_cast<uint32_t*>(o));
+            }
+          }
+          m = m_new;
+        }
+        // P = 2^(scale s - scale m) to TMEM, eight words at a time and one run behind; the row's sum
         const float base = m == -INFINITY ? 0.f : -m * a.scale_log2;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
+        float part[4] = {0.f, 0.f, 0.f, 0.f};
         uint32_t pw[2][kRun];
 #pragma unroll
         for (int c = 0; c <= 64 / kRun; ++c) {
@@ -358,49 +400,22 @@ __global__ void __launch_bounds__(kThreads, 1)
               fma2(p0, p1, s[2 * kRun * c + 2 * x], s[2 * kRun * c + 2 * x + 1], a.scale_log2, base);
               p0 = ex2_approx(p0);
               p1 = ex2_approx(p1);
-              add2(sum[2 * (x & 1)], sum[2 * (x & 1) + 1], p0, p1);
+              add2(part[2 * (x & 1)], part[2 * (x & 1) + 1], p0, p1);
               pw[c & 1][x] = E::pack(p0, p1);
             }
           }
-          if (c == 1 && wait_p) {
-            // the products of the step before have read P
-            ok = wait_on(&sh.v[half], parity ^ 1, sh, a.status) && ok;
-            __syncwarp();
-            tc5_fence_after();
-          }
-          if (c > 0) tc5_st8(p_col + kRun * (c - 1), pw[(c - 1) & 1]);
+          if (c > 0) tc5_st8(s_at + kRun * (c - 1), pw[(c - 1) & 1]);
         }
-        return (sum[0] + sum[1]) + (sum[2] + sum[3]);
-      };
-      if (cut) hide();
-      if (j < stride && in) m = maximum();
-      float sum = weights(C::kApart && j >= stride);
-      if (__any_sync(kFull, (in && (!(sum <= kMostSum) || m == -INFINITY)) || bad)) {
-        // some row's maximum has grown: O and l follow it, and P is made again (it has not been handed over)
-        if (bad) hide();
-        const float m_new = in ? fmaxf(m, maximum()) : m;
-        const float f = m_new == m ? 1.f : ex2_approx((m - m_new) * a.scale_log2);
-        l *= f;
-        m = m_new;
-        if (j >= stride) {
-          // the products into O before this step are complete
-#pragma unroll
-          for (int c = 0; c < D / 16; ++c) {
-            float o[16];
-            tc5_ld16(reinterpret_cast<uint32_t*>(o), o_col + 16 * c);
-            tc5_wait_ld();
-#pragma unroll
-            for (int x = 0; x < 16; ++x) o[x] *= f;
-            tc5_st16(o_col + 16 * c, reinterpret_cast<uint32_t*>(o));
-          }
-        }
-        sum = weights(false);
+        sum = (part[0] + part[1]) + (part[2] + part[3]);
+        if (turn || j < stride) break;
+        grow = __any_sync(kFull, in && (!(sum <= kMostSum) || m == -INFINITY));
+        if (!grow) break;                                          // else P is made again (it has not been handed over)
       }
       l += sum;
       tc5_wait_st();
       tc5_fence_before();
       __syncwarp();
-      if (lane == 0) mbar_arrive(smem_u32(&sh.p[half]));
+      if (lane == 0) mbar_arrive(smem_u32(&sh.p[C::kAhead ? j & 1 : half]));
     }
     // ------------------------------------------------------------- outputs
     if (act) {
@@ -424,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           sh.x[0][row] = m;
           sh.x[1][row] = l;
         }
-        named_sync<kSoftmaxThreads>(2);
+        named_sync<C::kSoftmaxThreads>(2);
         const float m1 = sh.x[0][row], l1 = sh.x[1][row], top = fmaxf(m, m1);
         f0 = m == -INFINITY ? 0.f : ex2_approx((m - top) * a.scale_log2);
         f1 = m1 == -INFINITY ? 0.f : ex2_approx((m1 - top) * a.scale_log2);
@@ -433,9 +448,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       const float inv = l > 0.f ? 1.0f / l : 0.f;
       const float row_lse = l > 0.f ? (m * a.scale_log2 + lg2_approx(l)) * kLn2 : -INFINITY;
-      const int64_t prow = int64_t(blockIdx.x) * 256 + (dual ? 0 : half * 128) + row;
+      const int prow = (dual ? 0 : half * 128) + row;
       if (in && !(dual && half == 1)) {
-        if (w.parts > 1) a.part_lse[prow] = row_lse;
+        if (w.parts > 1) a.part_lse[int64_t(blockIdx.x) * C::kRows + prow] = row_lse;
         else if (a.lse) a.lse[orow] = row_lse;
       }
       f0 *= inv;
@@ -455,9 +470,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (w.parts > 1) {
           if (in) {
-            float4* dst = reinterpret_cast<float4*>(a.part_o + prow * D + 32 * c);
+            float4* dst = a.part_o + (int64_t(blockIdx.x) * (D / 4) + 8 * c) * C::kRows + prow;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) dst[x] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
+            for (int x = 0; x < 8; ++x) dst[x * C::kRows] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
         } else {
           // through the half's query rows in shared memory (every product with them is complete), so that a store
@@ -485,31 +500,38 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc5_fence_before();
     }
   } else {
-  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(kOtherRegs));
-  if (warp == kMmaWarp) {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(C::kOtherRegs));
+  if (warp == C::kMmaWarp) {
     // ------------------------------------------------------------- products, issued by one thread
     if (steps > 0 && elect_one()) {
-      constexpr uint32_t id_s = tc5_idesc(kBf16, 128, kKeys, false), id_o = tc5_idesc(kBf16, 128, D, true);
+      constexpr uint32_t id_s2 = tc5_idesc(kBf16, 128, kKeys / 2, false), id_s = tc5_idesc(kBf16, 128, kKeys, false), id_o = tc5_idesc(kBf16, 128, D, true);
       const uint64_t q_desc = tc5_desc(smem_u32(smem), 16, 1024);
       const uint64_t k_desc = tc5_desc(smem_u32(ring), 16, C::kGroupBytes);
       const uint64_t v_desc = tc5_desc(smem_u32(ring), 1024, C::kGroupBytes);
-      auto scores = [&](int half, int slot) {                       // S = Q K^T
+      auto scores = [&](int half, int slot, int block) {                       // S = Q K^T
         const uint64_t qd = q_desc + (dual ? 0u : uint32_t(half * C::kSlotBytes / 16));
         const uint64_t kd = k_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < D / 16; ++kk) {
           const uint32_t q_at = (kk >> 2) * (128 * 128) + (kk & 3) * 32, k_at = (kk >> 2) * 1024 + (kk & 3) * 32;
-          tc5_mma_ss(tmem + half * 128, qd + q_at / 16, kd + k_at / 16, id_s, kk > 0);
+          if (!C::kAhead) {
+            tc5_mma_ss(tmem + half * 128, qd + q_at / 16, kd + k_at / 16, id_s, kk > 0);
+          } else if (block < 2) {
+            tc5_mma_ss(tmem + 64 * block, qd + q_at / 16, kd + k_at / 16, id_s, kk > 0);
+          } else {                                                  // blocks 2 and 0
+            tc5_mma_ss(tmem + 128, qd + q_at / 16, kd + k_at / 16, id_s2, kk > 0);
+            tc5_mma_ss(tmem, qd + q_at / 16, kd + (k_at + 8 * C::kGroupBytes) / 16, id_s2, kk > 0);
+          }
         }
         tc5_commit(smem_u32(&sh.s[half]));
       };
-      auto outputs = [&](int half, int slot, bool add, uint32_t parity) {   // O += P V once P is there
-        if (!wait_on(&sh.p[half], parity, sh, a.status)) return false;
+      auto outputs = [&](int half, int slot, bool add, int turn, uint32_t parity, int block) {   // O += P V once P is there
+        if (!wait_on(&sh.p[turn], parity, sh, a.status)) return false;
         tc5_fence_after();
         const uint64_t vd = v_desc + uint32_t(slot * C::kSlotBytes / 16);
 #pragma unroll
         for (int kk = 0; kk < kKeys / 16; ++kk)
-          tc5_mma_ts(tmem + C::kOCol + half * D, tmem + C::kPCol + half * C::kPStride + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
+          tc5_mma_ts(tmem + C::kOCol + half * D, tmem + (C::kAhead ? 64 * block : half * 128) + kk * 8, vd + uint32_t(kk * 2 * C::kGroupBytes / 16), id_o,
                      add || kk > 0);
         return true;
       };
@@ -522,42 +544,42 @@ __global__ void __launch_bounds__(kThreads, 1)
       // keys of step j are copy 2j of the ring, its values copy 2j + 1
       bool ok = wait_on(&sh.q, 0, sh, a.status) && wait_full(0);
       if (ok) {
-        scores(0, 0);
-        if (two) scores(1, 0);
+        scores(0, 0, 0);
+        if (two) scores(1, 0, 0);
         release(0);
       }
       if (ok && dual && (ok = wait_full(2))) {
-        scores(1, 2 % C::kSlots);
+        scores(1, 2 % C::kSlots, 0);
         release(2);
       }
-      // S of the next step of a half, once the half has read the one before (P apart)
-      auto ahead = [&](int half, int seq, uint32_t parity) {
-        if (!wait_full(seq) || !wait_on(&sh.r[half], parity, sh, a.status)) return false;
-        tc5_fence_after();
-        scores(half, seq % C::kSlots);
-        return true;
-      };
-      auto done = [&](int half, bool more) {
-        if (!more) tc5_commit(smem_u32(&sh.o[half]));
-        else if (C::kApart) tc5_commit(smem_u32(&sh.v[half]));
-      };
       if (dual) {
         for (int j = 0; ok && j < steps; ++j) {
           const int half = j & 1, sv = 2 * j + 1, sk = 2 * j + 4;
-          const uint32_t parity = (j >> 1) & 1;
-          const bool more = j + 2 < steps;
-          if (C::kApart && more) {
-            if (!(ok = ahead(half, sk, parity))) break;
-            release(sk);
-          }
-          if (!(ok = wait_full(sv) && outputs(half, sv % C::kSlots, j > 1, parity))) break;
+          if (!(ok = wait_full(sv) && outputs(half, sv % C::kSlots, j > 1, half, (j >> 1) & 1, 0))) break;
           release(sv);
-          done(half, more);
-          if (!C::kApart && more && (ok = wait_full(sk))) {
-            scores(half, sk % C::kSlots);
+          if (j + 2 >= steps) {
+            tc5_commit(smem_u32(&sh.o[half]));
+          } else if ((ok = wait_full(sk))) {
+            scores(half, sk % C::kSlots, 0);
             release(sk);
           }
         }
+      } else if (C::kAhead) {
+        int block = 0, next = 1;
+        for (int j = 0; ok && j < steps; ++j) {
+          const int sv = 2 * j + 1, sk = 2 * j + 2;
+          if (j + 1 < steps) {                                      // S of the next step, once this one's is read
+            if (!(ok = wait_full(sk) && wait_on(&sh.r, j & 1, sh, a.status))) break;
+            tc5_fence_after();
+            scores(0, sk % C::kSlots, next);
+            release(sk);
+          }
+          if (!(ok = wait_full(sv) && outputs(0, sv % C::kSlots, j > 0, j & 1, (j >> 1) & 1, block))) break;
+          release(sv);
+          tc5_commit(smem_u32(&sh.v));
+          block = next, next = next < 2 ? next + 1 : 0;
+        }
+        if (ok) tc5_commit(smem_u32(&sh.o[0]));
       } else {
         for (int j = 0; ok && j < steps; ++j) {
           const int sv = 2 * j + 1, sk = 2 * j + 2;
@@ -565,19 +587,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
           for (int half = 0; half < 2; ++half) {
             if (half && !two) break;
-            if (C::kApart && more && !(ok = ahead(half, sk, j & 1))) break;
             if (half == 0 && !(ok = wait_full(sv))) break;
-            if (!(ok = outputs(half, sv % C::kSlots, j > 0, j & 1))) break;
-            done(half, more);
-            if (!C::kApart && more) {
-              if (half == 1 || !two) release(sv);
+            if (!(ok = outputs(half, sv % C::kSlots, j > 0, half, j & 1, 0))) break;
+            if (half == 1 || !two) release(sv);
+            if (!more) {
+              tc5_commit(smem_u32(&sh.o[half]));
+            } else {
               if (half == 0 && !(ok = wait_full(sk))) break;
-              scores(half, sk % C::kSlots);
+              scores(half, sk % C::kSlots, 0);
             }
           }
-          if (!ok) break;
-          if (C::kApart || !more) release(sv);
-          if (more) release(sk);
+          if (ok && more) release(sk);
         }
       }
       if (!ok) {                                                    // let what was issued finish
@@ -586,10 +606,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     }
     __syncwarp();
-  } else if (warp <= kMmaWarp + C::kProducers) {
+  } else if (warp <= C::kMmaWarp + C::kProducers) {
     // ------------------------------------------------------------- copies
     constexpr int kCopyThreads = 32 * C::kProducers;
-    const int ct = threadIdx.x - 32 * (kMmaWarp + 1);
+    const int ct = threadIdx.x - 32 * (C::kMmaWarp + 1);
     auto copy_sync = [&]() {
       if (C::kProducers == 1) __syncwarp();
       else named_sync<kCopyThreads>(1);
@@ -772,57 +792,84 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   }
   __syncthreads();
-  if (warp == kMmaWarp) {
+  if (warp == C::kMmaWarp) {
     tc5_fence_after();
-    tc5_dealloc(tmem, 512);
+    tc5_dealloc(tmem, C::kCols);
   }
-  if (w.parts == 1 || warp >= kMmaWarp) return;
+  if (w.parts == 1 || warp >= C::kMmaWarp) return;
 
   // ------------------------------------------------------------- merge the parts of the unit
   if (threadIdx.x == 0) sh.last = ticket(&a.tickets[w.unit]) == w.parts - 1;
-  named_sync<kSoftmaxThreads>(2);
+  named_sync<C::kSoftmaxThreads>(2);
   if (!sh.last) return;
-  const int64_t part0 = (int64_t(blockIdx.x) - w.part) * 256;
-  const int rows = two ? 256 : 128;
-  for (int i = threadIdx.x; i < rows * (D / 4); i += kSoftmaxThreads) {
-    // a thread merges four columns of a row, four parts in flight, in the order of the parts
-    const int r = i / (D / 4), d = 4 * (i % (D / 4));
-    const int t = (r >> 7) * half_tokens + (r & 127) / G;
-    if ((r & 127) / G >= half_tokens || t >= nt) continue;
-    const int64_t orow = int64_t(w.c0 + t0 + t) * a.H_q + int64_t(h) * G + (r & 127) % G;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    float M = -INFINITY, tot = 0.f;
-    for (int p0 = 0; p0 < w.parts; p0 += 4) {
-      float4 x[4];
-      float z[4];
+  // A warp merges 8 rows x 32 columns (eight a lane), two such at once, four parts in flight, in the order of the parts.
+  constexpr int kWide = D / 32, kAtOnce = 2;
+  const int64_t part0 = int64_t(blockIdx.x) - w.part;
+  const int tiles = (two ? 256 : 128) / 8 * kWide;
+  for (int g0 = warp; g0 < tiles; g0 += kAtOnce * C::kMmaWarp) {
+    float acc[kAtOnce][8], M[kAtOnce], tot[kAtOnce];
+    int64_t orow[kAtOnce];
+    int r[kAtOnce], c8[kAtOnce];                                   // row, chunk of eight columns
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        z[k] = -INFINITY;
-        if (p0 + k < w.parts) {
-          const int64_t at = part0 + (p0 + k) * 256 + r;
-          z[k] = __ldcg(a.part_lse + at);
-          x[k] = __ldcg(reinterpret_cast<const float4*>(a.part_o + at * D + d));
+    for (int u = 0; u < kAtOnce; ++u) {
+      const int g = g0 + u * C::kMmaWarp;
+      r[u] = g / kWide * 8 + (lane & 7), c8[u] = g % kWide * 4 + (lane >> 3);
+      const int t = (r[u] >> 7) * half_tokens + (r[u] & 127) / G;
+      orow[u] = g < tiles && (r[u] & 127) / G < half_tokens && t < nt
+                    ? int64_t(w.c0 + t0 + t) * a.H_q + int64_t(h) * G + (r[u] & 127) % G
+                    : -1;
+      M[u] = -INFINITY, tot[u] = 0.f;
+#pragma unroll
+      for (int x = 0; x < 8; ++x) acc[u][x] = 0.f;
+    }
+    if (!__any_sync(kFull, orow[0] >= 0 || orow[kAtOnce - 1] >= 0)) continue;
+    for (int p0 = 0; p0 < w.parts; p0 += 4) {
+      float4 x[kAtOnce][4][2];
+      float z[kAtOnce][4];
+#pragma unroll
+      for (int u = 0; u < kAtOnce; ++u) {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          z[u][k] = -INFINITY;
+          x[u][k][0] = x[u][k][1] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (orow[u] >= 0 && p0 + k < w.parts) {
+            const float4* src = a.part_o + ((part0 + p0 + k) * (D / 4) + 2 * c8[u]) * C::kRows + r[u];
+            z[u][k] = __ldcg(a.part_lse + (part0 + p0 + k) * C::kRows + r[u]);
+            x[u][k][0] = __ldcg(src);
+            x[u][k][1] = __ldcg(src + C::kRows);
+          }
         }
       }
-      const float top = fmaxf(M, fmaxf(fmaxf(z[0], z[1]), fmaxf(z[2], z[3])));
-      const float f = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLog2e);
-      tot *= f, acc.x *= f, acc.y *= f, acc.z *= f, acc.w *= f;
-      M = top;
 #pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (z[k] == -INFINITY) continue;                           // an empty part
-        const float g = ex2_approx((z[k] - M) * kLog2e);
-        tot += g;
-        acc.x = fmaf(g, x[k].x, acc.x);
-        acc.y = fmaf(g, x[k].y, acc.y);
-        acc.z = fmaf(g, x[k].z, acc.z);
-        acc.w = fmaf(g, x[k].w, acc.w);
+      for (int u = 0; u < kAtOnce; ++u) {
+        const float top = fmaxf(M[u], fmaxf(fmaxf(z[u][0], z[u][1]), fmaxf(z[u][2], z[u][3])));
+        const float f = M[u] == -INFINITY ? 0.f : ex2_approx((M[u] - top) * kLog2e);
+        M[u] = top;
+        tot[u] *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc[u][i] *= f;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float e = z[u][k] == -INFINITY ? 0.f : ex2_approx((z[u][k] - top) * kLog2e);   // 0: an empty part
+          const float v[8] = {x[u][k][0].x, x[u][k][0].y, x[u][k][0].z, x[u][k][0].w,
+                              x[u][k][1].x, x[u][k][1].y, x[u][k][1].z, x[u][k][1].w};
+          tot[u] += e;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) acc[u][i] = fmaf(e, v[i], acc[u][i]);
+        }
       }
     }
-    const float f = tot > 0.f ? 1.0f / tot : 0.f;
-    *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + orow * D + d) =
-        make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
-    if (a.lse && d == 0) a.lse[orow] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+#pragma unroll
+    for (int u = 0; u < kAtOnce; ++u) {
+      if (orow[u] < 0) continue;
+      const float f = tot[u] > 0.f ? 1.0f / tot[u] : 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) acc[u][i] *= f;
+      *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow[u] * D + 8 * c8[u]) =
+          make_uint4(E::pack(acc[u][0], acc[u][1]), E::pack(acc[u][2], acc[u][3]), E::pack(acc[u][4], acc[u][5]),
+                     E::pack(acc[u][6], acc[u][7]));
+      if (a.lse && c8[u] == 0) a.lse[orow[u]] = tot[u] > 0.f ? M[u] + lg2_approx(tot[u]) * kLn2 : -INFINITY;
+    }
   }
   if (threadIdx.x == 0) a.tickets[w.unit] = 0;
 }
@@ -830,11 +877,14 @@ __global__ void __launch_bounds__(kThreads, 1)
 size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
 
 // Items of a call: at most one partly filled one per request.
-int64_t items_of(int64_t tokens, int batch, int G) { return tokens / (2 * (128 / G)) + batch; }
+int64_t items_of(int64_t tokens, int batch, int G, int D) { return tokens / (ways(D) * (128 / G)) + batch; }
 
 // Items are cut into parts where they would leave half of the SMs idle (three
 // requests a lane are looked over then).
-bool splits(int64_t units, int batch, int sms) { return 2 * units <= sms && batch <= 96; }
+bool splits(int64_t units, int batch, int ctas) { return 2 * units <= ctas && batch <= 96; }
+
+// CTAs that run at once.
+int resident(int D) { return sm_count() * (3 - ways(D)); }
 
 struct WsLayout {
   size_t part_lse, part_o, total;
@@ -842,8 +892,8 @@ struct WsLayout {
 WsLayout ws_layout(int64_t ctas, int D) {
   WsLayout w;
   w.part_lse = align256(size_t(ctas) * 4);
-  w.part_o = w.part_lse + size_t(ctas) * 256 * 4;
-  w.total = w.part_o + size_t(ctas) * 256 * D * 4;
+  w.part_o = w.part_lse + size_t(ctas) * 128 * ways(D) * 4;
+  w.total = w.part_o + size_t(ctas) * 128 * ways(D) * D * 4;
   return w;
 }
 
@@ -855,8 +905,8 @@ sa_status launch(const PagedPrefillArgs& a, cudaStream_t s, const CUtensorMap& m
   auto k = paged_prefill_kernel<T, D, kTma>;
   constexpr int smem = Cfg<D, kTma>::kSharedAt + int(sizeof(Shared));
   if (!ensure_smem(k, smem, cache)) return SA_ERR_CUDA;
-  const unsigned ctas = a.split ? unsigned(sm_count()) : unsigned(a.items) * a.H_kv;
-  return launch_ex(k, dim3(ctas), dim3(kThreads), smem, s, false, 1, a, mq, mk, mv) == cudaSuccess
+  const unsigned ctas = a.split ? unsigned(resident(D)) : unsigned(a.items) * a.H_kv;
+  return launch_ex(k, dim3(ctas), dim3(Cfg<D, kTma>::kThreads), smem, s, false, 1, a, mq, mk, mv) == cudaSuccess
              ? SA_OK
              : SA_ERR_CUDA;
 }
@@ -880,7 +930,7 @@ extern "C" size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_
       num_q_heads % num_kv_heads)
     return 0;
   // a call of few tokens has an item per request: what it needs, calls of more tokens need at most
-  return splits(int64_t(batch) * num_kv_heads, batch, sm_count()) ? ws_layout(sm_count(), head_dim).total : 256;
+  return splits(int64_t(batch) * num_kv_heads, batch, resident(head_dim)) ? ws_layout(resident(head_dim), head_dim).total : 256;
 }
 
 extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
@@ -908,16 +958,16 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
   // a window of the table's length hides nothing
   a.window = window < int64_t(batch->bt_stride) * cache->page_size ? window : 0;
   a.scale_log2 = (scale > 0.f ? scale : 1.0f / sqrtf(float(D))) * kLog2e;
-  const int64_t items = items_of(num_tokens, batch->batch, G), units = items * H;
+  const int64_t items = items_of(num_tokens, batch->batch, G, D), units = items * H;
   if (units > 0x7fffffff) return SA_ERR_UNSUPPORTED;
   a.items = int(items);
-  a.split = splits(units, batch->batch, sm_count());
+  a.split = splits(units, batch->batch, resident(D));
   if (a.split) {
-    const WsLayout w = ws_layout(sm_count(), D);
+    const WsLayout w = ws_layout(resident(D), D);
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     a.tickets = reinterpret_cast<int32_t*>(ws);
     a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-    a.part_o = reinterpret_cast<float*>(ws + w.part_o);
+    a.part_o = reinterpret_cast<float4*>(ws + w.part_o);
   }
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SA_BF16;

@@ -343,6 +343,27 @@ def test_prefill_scores_far_apart_and_equal():
     _prefill(p, [300], q=q.abs())
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("new", [700, 3])
+def test_prefill_scores_that_rise_along_the_cache(dtype, D, new):
+    # the reference of the softmax has to follow every few steps, in whole items and in parts
+    p = Problem([1500, 1301], Hkv=1, G=4, D=D, dtype=dtype)
+    for b, n in enumerate(p.lens):
+        ramp = torch.linspace(0, 3, n, device="cuda")[:, None, None]
+        p.seqs[b][0] = (ramp * torch.ones_like(p.seqs[b][0])).to(p.dt)
+        for j in range(n):
+            p.k[int(p.table[b, j // 16]), :, j % 16] = p.seqs[b][0][j]
+    q = p.rand(2 * new, 4, D, scale=2.0).abs()
+    _prefill(p, [new, new], q=q)
+    _prefill(p, [new, new], q=q, window=400, n_sink=3)
+
+
+def test_prefill_of_more_items_than_run_at_once():
+    _prefill(Problem([3000, 33, 0, 1200], Hkv=8, G=7, D=64, ps=32), [2999, 30, 0, 5])
+    _prefill(Problem([1900, 700], Hkv=8, G=5, D=64, ps=4), [1500, 700], window=333, n_sink=2)
+
+
 def test_prefill_bad_data_is_flagged():
     p = Problem([100, 50, 40], Hkv=1, G=2)
     q = p.rand(12, 2, 128)
