@@ -48,6 +48,7 @@ constexpr int kRun = 8;                   // words of P stored at a time
 // Steps of a part at least, and of an item that is cut at all: a merge costs about six. Measured (us): 30 tokens x 64
 // heads over 500, 5 steps, whole 15 and in parts 22; over 2000, 16 steps, parts of 4 24 and of 6 28.
 constexpr int kMinPart = 4, kMinCut = 9;
+constexpr int kTailPart = 16, kMostTail = 8;   // steps at least and number at most of the parts of a unit behind the last full round
 constexpr int kLag = 2;                   // row-by-row copies under way behind the newest
 
 struct PagedPrefillArgs {
@@ -63,6 +64,7 @@ struct PagedPrefillArgs {
   int32_t* tickets;     // [units]
   int32_t* status;
   int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink, items, split;
+  int whole, tail_parts;  // without split: CTAs before the last units, and parts of each of those
   float scale_log2;
 };
 
@@ -95,7 +97,7 @@ struct Cfg {
 
 // What a CTA does: tokens [t0, t0 + nt) of request b for KV head h, steps [tb, tb + steps) of the visible keys.
 struct Work {
-  int b, item, h, part, parts, unit, c0, n, L;
+  int b, item, h, part, parts, unit, slot, c0, n, L;   // unit, slot: of the tickets and of the parts' results
 };
 
 struct Shared {
@@ -159,9 +161,19 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, in
   const int lane = threadIdx.x & 31;
   if (!a.split) {
     // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
-    w.h = blockIdx.x / a.items;
-    w.part = 0, w.parts = 1, w.unit = 0;
-    return find_item(a.new_cu, a.seq_lens, a.batch, per, a.items - 1 - blockIdx.x % a.items, w.b, w.item, w.c0, w.n, w.L);
+    const int tail = max(0, int(blockIdx.x) - a.whole);
+    w.parts = int(blockIdx.x) < a.whole ? 1 : a.tail_parts;
+    w.part = tail % w.parts, w.unit = tail / w.parts, w.slot = tail;
+    const int u = min(int(blockIdx.x), a.whole) + w.unit;
+    w.h = u / a.items;
+    if (!find_item(a.new_cu, a.seq_lens, a.batch, per, a.items - 1 - u % a.items, w.b, w.item, w.c0, w.n, w.L)) return false;
+    if (w.parts > 1) {
+      const int t0 = w.item * per, first = w.L - w.n + t0;
+      const int steps = Span<kKeys>(first, first + min(per, w.n - t0) - 1, min(max(w.L, 0), cap), a.window, a.n_sink).tiles;
+      w.parts = max(1, min(w.parts, steps / kTailPart));
+      if (w.part >= w.parts) return false;
+    }
+    return true;
   }
   // Every (item, head) of request b in ceil(steps_b / chunk) parts, chunk the least
   // that gives no more parts than CTAs. At most 96 requests (three a lane).
@@ -217,7 +229,7 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, in
       w.parts = __shfl_sync(kFull, np, k);
       const int at = int(blockIdx.x) - first, unit = at / w.parts;
       w.part = at % w.parts;
-      w.unit = unit0 + unit;
+      w.unit = unit0 + unit, w.slot = int(blockIdx.x);
       w.h = unit % a.H_kv, w.item = unit / a.H_kv, w.b = 32 * i + k;
       w.c0 = __shfl_sync(kFull, c0[i], k), w.n = __shfl_sync(kFull, n[i], k), w.L = __shfl_sync(kFull, L[i], k);
       return true;
@@ -450,7 +462,7 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
       const float row_lse = l > 0.f ? (m * a.scale_log2 + lg2_approx(l)) * kLn2 : -INFINITY;
       const int prow = (dual ? 0 : half * 128) + row;
       if (in && !(dual && half == 1)) {
-        if (w.parts > 1) a.part_lse[int64_t(blockIdx.x) * C::kRows + prow] = row_lse;
+        if (w.parts > 1) a.part_lse[int64_t(w.slot) * C::kRows + prow] = row_lse;
         else if (a.lse) a.lse[orow] = row_lse;
       }
       f0 *= inv;
@@ -470,7 +482,7 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
         }
         if (w.parts > 1) {
           if (in) {
-            float4* dst = a.part_o + (int64_t(blockIdx.x) * (D / 4) + 8 * c) * C::kRows + prow;
+            float4* dst = a.part_o + (int64_t(w.slot) * (D / 4) + 8 * c) * C::kRows + prow;
 #pragma unroll
             for (int x = 0; x < 8; ++x) dst[x * C::kRows] = make_float4(o[4 * x], o[4 * x + 1], o[4 * x + 2], o[4 * x + 3]);
           }
@@ -804,7 +816,7 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
   if (!sh.last) return;
   // A warp merges 8 rows x 32 columns (eight a lane), two such at once, four parts in flight, in the order of the parts.
   constexpr int kWide = D / 32, kAtOnce = 2;
-  const int64_t part0 = int64_t(blockIdx.x) - w.part;
+  const int64_t part0 = w.slot - w.part;
   const int tiles = (two ? 256 : 128) / 8 * kWide;
   for (int g0 = warp; g0 < tiles; g0 += kAtOnce * C::kMmaWarp) {
     float acc[kAtOnce][8], M[kAtOnce], tot[kAtOnce];
@@ -905,7 +917,7 @@ sa_status launch(const PagedPrefillArgs& a, cudaStream_t s, const CUtensorMap& m
   auto k = paged_prefill_kernel<T, D, kTma>;
   constexpr int smem = Cfg<D, kTma>::kSharedAt + int(sizeof(Shared));
   if (!ensure_smem(k, smem, cache)) return SA_ERR_CUDA;
-  const unsigned ctas = a.split ? unsigned(resident(D)) : unsigned(a.items) * a.H_kv;
+  const unsigned ctas = a.split ? unsigned(resident(D)) : unsigned(a.whole + (a.items * a.H_kv - a.whole) * a.tail_parts);
   return launch_ex(k, dim3(ctas), dim3(Cfg<D, kTma>::kThreads), smem, s, false, 1, a, mq, mk, mv) == cudaSuccess
              ? SA_OK
              : SA_ERR_CUDA;
@@ -929,8 +941,7 @@ extern "C" size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_
   if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_tokens < 0 ||
       num_q_heads % num_kv_heads)
     return 0;
-  // a call of few tokens has an item per request: what it needs, calls of more tokens need at most
-  return splits(int64_t(batch) * num_kv_heads, batch, resident(head_dim)) ? ws_layout(resident(head_dim), head_dim).total : 256;
+  return ws_layout(resident(head_dim), head_dim).total;           // a part each of the CTAs that run at once
 }
 
 extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
@@ -962,13 +973,20 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
   if (units > 0x7fffffff) return SA_ERR_UNSUPPORTED;
   a.items = int(items);
   a.split = splits(units, batch->batch, resident(D));
-  if (a.split) {
-    const WsLayout w = ws_layout(resident(D), D);
-    uint8_t* ws = static_cast<uint8_t*>(workspace);
-    a.tickets = reinterpret_cast<int32_t*>(ws);
-    a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
-    a.part_o = reinterpret_cast<float4*>(ws + w.part_o);
-  }
+  // The units behind the last full round of CTAs in parts that fill one more, where the table and the window leave room
+  // for two parts' keys. Measured (us) without / with: a chunk of 2048 tokens x 64 heads behind 64000 (512 units) 2730 /
+  // 2510, three requests of 700 - 900 behind 3000 - 4500 153 / 147; five of 100 - 900 behind 300 - 1500, whose parts would
+  // all be empty, 65.5 / 68.
+  const int ctas = resident(D), rest = int(units % ctas);
+  const int64_t keys = min(int64_t(batch->bt_stride) * cache->page_size,
+                           a.window > 0 ? int64_t(a.window) + n_sink : int64_t(0x7fffffff));
+  a.tail_parts = !a.split && rest && keys >= 2 * kTailPart * kKeys ? max(1, min(ctas / rest, kMostTail)) : 1;
+  a.whole = int(a.tail_parts > 1 ? units - rest : units);
+  const WsLayout w = ws_layout(ctas, D);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  a.tickets = reinterpret_cast<int32_t*>(ws);
+  a.part_lse = reinterpret_cast<float*>(ws + w.part_lse);
+  a.part_o = reinterpret_cast<float4*>(ws + w.part_o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool bf = cache->dtype == SA_BF16;
   if (D == 128)

@@ -359,6 +359,17 @@ def test_prefill_scores_that_rise_along_the_cache(dtype, D, new):
     _prefill(p, [new, new], q=q, window=400, n_sink=3)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("window", [0, 4200])
+def test_prefill_items_behind_the_last_full_round(D, window):
+    # 8 heads x 16 queries: 168 (328 at head dim 64) items, the last of them, of the last head, in parts
+    p = Problem([5000], Hkv=8, G=16, D=D)
+    q, out, lse, ws = _prefill(p, [320], window=window, n_sink=window and 5)
+    again = _prefill(p, [320], window=window, n_sink=window and 5, q=q, ws=ws)
+    assert torch.equal(again[1], out) and torch.equal(again[2], lse)
+    _prefill(Problem([700, 4500, 40], Hkv=8, G=16, D=D), [40, 290, 1], window=window, ws=ws)
+
+
 def test_prefill_of_more_items_than_run_at_once():
     _prefill(Problem([3000, 33, 0, 1200], Hkv=8, G=7, D=64, ps=32), [2999, 30, 0, 5])
     _prefill(Problem([1900, 700], Hkv=8, G=5, D=64, ps=4), [1500, 700], window=333, n_sink=2)
