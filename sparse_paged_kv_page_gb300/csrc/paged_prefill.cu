@@ -21,7 +21,8 @@
 // times what a freed page holds must be 0), key rows masked.
 //
 // Bound by the tensor cores for prompts (16384 tokens, 32 / 8 heads of 128, pages of 16:
-// 1310 us, 1.68 PFLOP/s, the power limit's rate for a dense product); at head dim 64 by
+// 1310 us, 1.68 PFLOP/s; 2048 tokens behind 64000, 64 / 8 heads, 2510 us, 1.73 PFLOP/s:
+// the rate that the power limit leaves a dense product); at head dim 64 by
 // the rows' turn from S to P and the number of page copies (an operation costs about 80
 // cycles whatever its size: a prompt of 8192 over 4096 in pages of 16 1145 us, of 128
 // 920); for a few rows over a long cache by HBM, where each item's keys are cut into
