@@ -668,8 +668,8 @@ size_t sa_paged_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32
  *            q itself
  *   scale    <= 0 selects head_dim ** -0.5
  *   lse      nullable float32 [batch, num_q_heads], natural log
- * Tokens that the query does not see are never used, whatever they hold. Pages
- * whose block id is out of range are skipped with SA_DEV_BAD_BLOCK; a request
+ * Tokens that the query does not see are never used, whatever they hold; a NaN in
+ * the query or in a key that it sees makes its out and lse NaN. Pages whose block id is out of range are skipped with SA_DEV_BAD_BLOCK; a request
  * longer than its table row is read up to the row's end with SA_DEV_OVERFLOW; a
  * negative length counts as 0 with SA_DEV_BAD_COUNT. Results do not depend on
  * timing: repeated calls give the same bits. Limits: batch <= 1024, num_q_heads /

@@ -285,10 +285,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
         f[w] = mw == -INFINITY ? 0.f : ex2_approx(mw - M);
         tot = fmaf(wl[w * 16 + row], f[w], tot);
       }
-      const float inv = tot > 0.f ? 1.0f / tot : 0.f;
+      const float inv = tot != 0.f ? 1.0f / tot : 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) s_sf[w][row] = f[w] * inv;
-      s_rl[row] = tot > 0.f ? (M + lg2_approx(tot)) * kLn2 : -INFINITY;
+      s_rl[row] = tot != 0.f ? (M + lg2_approx(tot)) * kLn2 : -INFINITY;
     }
     __syncthreads();
     auto merged = [&](int row, int d) {
@@ -362,9 +362,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             mine[0] = M, mine[1] = tot, mine[2] = acc.x, mine[3] = acc.y, mine[4] = acc.z, mine[5] = acc.w;
             continue;
           }
-          const float f = tot > 0.f ? 1.0f / tot : 0.f;
+          const float f = tot != 0.f ? 1.0f / tot : 0.f;
           *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
-          if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+          if (a.lse && idx % D == 0) a.lse[row0 + row] = tot != 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
         }
         if (ways > 1) {
           __syncthreads();
@@ -382,9 +382,9 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
               acc.z = fmaf(w, x[4], acc.z);
               acc.w = fmaf(w, x[5], acc.w);
             }
-            const float f = tot > 0.f ? 1.0f / tot : 0.f;
+            const float f = tot != 0.f ? 1.0f / tot : 0.f;
             *reinterpret_cast<uint2*>(outp + idx) = make_uint2(E::pack(acc.x * f, acc.y * f), E::pack(acc.z * f, acc.w * f));
-            if (a.lse && idx % D == 0) a.lse[row0 + row] = tot > 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
+            if (a.lse && idx % D == 0) a.lse[row0 + row] = tot != 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
           }
         }
         if (threadIdx.x == 0) a.tickets[unit] = 0;

@@ -375,12 +375,14 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
         return fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
       };
       if (cut || bad) hide();
-      float sum;
-      bool grow = j < stride;                                      // the reference follows the row's maximum
+      float sum = INFINITY;                                        // (of the first step, before it is known)
+      bool grow = j < stride;                                      // some row's reference follows its maximum
 #pragma unroll 1
       for (int turn = 0;; ++turn) {
         if (grow) {
-          const float m_new = in ? fmaxf(m, maximum()) : m;
+          // this row's: where its own sum says so, so that a result does not depend on the rows beside it
+          const float top = maximum();
+          const float m_new = in && (sum > kMostSum || sum != sum || m == -INFINITY) ? fmaxf(m, top) : m;
           if (j >= stride) {
             // O and l follow; the products into O before this step are complete
             if (C::kAhead) ok = wait_on(&sh.v, parity ^ 1, sh, a.status) && ok;
@@ -459,8 +461,8 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
         l = l * f0 + l1 * f1;
         m = top;
       }
-      const float inv = l > 0.f ? 1.0f / l : 0.f;
-      const float row_lse = l > 0.f ? (m * a.scale_log2 + lg2_approx(l)) * kLn2 : -INFINITY;
+      const float inv = l != 0.f ? 1.0f / l : 0.f;
+      const float row_lse = l != 0.f ? (m * a.scale_log2 + lg2_approx(l)) * kLn2 : -INFINITY;
       const int prow = (dual ? 0 : half * 128) + row;
       if (in && !(dual && half == 1)) {
         if (w.parts > 1) a.part_lse[int64_t(w.slot) * C::kRows + prow] = row_lse;
@@ -478,8 +480,8 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
         tc5_wait_ld();
 #pragma unroll
         for (int x = 0; x < 32; ++x) {
-          o[x] = l > 0.f ? o[x] * f0 : 0.f;
-          if (dual && l > 0.f) o[x] = fmaf(other[(32 * c + x) * kKeys + row], f1, o[x]);
+          o[x] = l != 0.f ? o[x] * f0 : 0.f;
+          if (dual && l != 0.f) o[x] = fmaf(other[(32 * c + x) * kKeys + row], f1, o[x]);
         }
         if (w.parts > 1) {
           if (in) {
@@ -875,13 +877,13 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
 #pragma unroll
     for (int u = 0; u < kAtOnce; ++u) {
       if (orow[u] < 0) continue;
-      const float f = tot[u] > 0.f ? 1.0f / tot[u] : 0.f;
+      const float f = tot[u] != 0.f ? 1.0f / tot[u] : 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) acc[u][i] *= f;
       *reinterpret_cast<uint4*>(static_cast<T*>(a.out) + orow[u] * D + 8 * c8[u]) =
           make_uint4(E::pack(acc[u][0], acc[u][1]), E::pack(acc[u][2], acc[u][3]), E::pack(acc[u][4], acc[u][5]),
                      E::pack(acc[u][6], acc[u][7]));
-      if (a.lse && c8[u] == 0) a.lse[orow[u]] = tot[u] > 0.f ? M[u] + lg2_approx(tot[u]) * kLn2 : -INFINITY;
+      if (a.lse && c8[u] == 0) a.lse[orow[u]] = tot[u] != 0.f ? M[u] + lg2_approx(tot[u]) * kLn2 : -INFINITY;
     }
   }
   if (threadIdx.x == 0) a.tickets[w.unit] = 0;

@@ -298,3 +298,40 @@ def test_binding_refuses_other_shapes_and_types():
     with pytest.raises(S.SaError):                                   # rot_dim 40
         S.sa_append_kv_rope(p.cache, p.batch, S.make_rope(S.rope_table(64, 40)), q, k, v, cu, 3, q)
     assert p.seq_lens.tolist() == [20]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ps", [4, 16])
+def test_nan_in_a_query_or_a_visible_key_shows(D, ps):
+    # never a silent 0: the rows that see it are NaN, the others as without it
+    import sparse_paged_kv_page_gb300 as S
+    lens, new = [3000, 50, 700], [40, 20, 3]
+    p = Problem(lens, Hkv=1, G=4, D=D, ps=ps)
+    qd, qp = p.rand(3, 4, D), p.rand(63, 4, D)
+    cu = torch.tensor([0, 40, 60, 63], dtype=torch.int32).cuda()
+
+    def run():
+        od, op = torch.empty_like(qd), torch.empty_like(qp)
+        ld, lp = (torch.empty(x.shape[:2], device="cuda") for x in (qd, qp))
+        S.sa_paged_decode(p.cache, p.batch, qd, 4, 0.0, od, lse=ld, workspace=S.alloc_paged_decode_workspace(3, 1, 4, D))
+        S.sa_paged_prefill(p.cache, p.batch, qp, 4, cu, 0.0, op, lse=lp,
+                           workspace=S.alloc_paged_prefill_workspace(3, 1, 4, D, 63))
+        torch.cuda.synchronize()
+        return od, ld, op, lp
+
+    want = run()
+    qd[1, 2, 5] = qp[7, 1, 3] = float("nan")
+    od, ld, op, lp = run()
+    for out, lse, at, o, l in ((od, ld, (1, 2), want[0], want[1]), (op, lp, (7, 1), want[2], want[3])):
+        assert bool(out[at].isnan().all()) and bool(lse[at].isnan())
+        rest = torch.ones(lse.shape, dtype=torch.bool, device="cuda")
+        rest[at] = False
+        assert torch.equal(out[rest], o[rest]) and torch.equal(lse[rest], l[rest])
+    qd[1, 2, 5] = qp[7, 1, 3] = 0.0
+    want = run()
+    j = 2980                                               # of request 0: its new tokens 20 .. 39 see it
+    p.k[int(p.table[0, j // ps]), 0, j % ps, 0] = float("nan")
+    od, ld, op, lp = run()
+    assert bool(od[0].isnan().all()) and torch.equal(od[1:], want[0][1:])
+    assert bool(op[20:40].isnan().all()) and bool(lp[20:40].isnan().all())
+    assert torch.equal(op[:20], want[2][:20]) and torch.equal(op[40:], want[2][40:])
