@@ -46,10 +46,14 @@ constexpr int kTileRing = 8;              // steps whose row masks are kept
 // maximum (60 instructions of 380 a row), the sum that is made anyway tells.
 constexpr float kMostSum = 8192.0f;
 constexpr int kRun = 8;                   // words of P stored at a time
-// Steps of a part at least, and of an item that is cut at all: a merge costs about six. Measured (us): 30 tokens x 64
-// heads over 500, 5 steps, whole 15 and in parts 22; over 2000, 16 steps, parts of 4 24 and of 6 28.
+// Steps of a part at least, and of an item that is cut at all: a merge costs about six. Measured (us) with items of two
+// halves: 30 tokens x 64 heads over 500, 5 steps, whole 15 and in parts 22; over 2000, 16 steps, parts of 4 24, of 6 28.
 constexpr int kMinPart = 4, kMinCut = 9;
 constexpr int kTailPart = 16, kMostTail = 8;   // steps at least and number at most of the parts of a unit behind the last full round
+// Steps of all items (64 KB of keys and values each) up to which they stay near, in L2, for a second reader: items of a
+// call in parts are of one half then. Measured (us), two halves / one: 30 tokens x 64 heads over 2000 24.5 / 19, 8000 49 /
+// 28, 32000 (2000 steps) 62 / 56, 120000 129 / 153, four requests over 16000 (3776 steps) 66 / 94.
+constexpr int kNear = 2048;
 constexpr int kLag = 2;                   // row-by-row copies under way behind the newest
 
 struct PagedPrefillArgs {
@@ -98,7 +102,7 @@ struct Cfg {
 
 // What a CTA does: tokens [t0, t0 + nt) of request b for KV head h, steps [tb, tb + steps) of the visible keys.
 struct Work {
-  int b, item, h, part, parts, unit, slot, c0, n, L;   // unit, slot: of the tickets and of the parts' results
+  int b, item, h, per, part, parts, unit, slot, c0, n, L;   // per: tokens of an item; unit, slot: of the tickets and of the parts' results
 };
 
 struct Shared {
@@ -158,8 +162,10 @@ __device__ __forceinline__ int request_steps(const PagedPrefillArgs& a, int L, i
 __device__ __forceinline__ int parts_of(int steps, int chunk) { return steps < kMinCut ? 1 : (steps + chunk - 1) / chunk; }
 
 // The CTA's work, found by one warp. False if there is none.
-__device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, int per, Work& w) {
+__device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, int half_tokens, int ways, Work& w) {
   const int lane = threadIdx.x & 31;
+  int per = ways * half_tokens;
+  w.per = per;
   if (!a.split) {
     // heads outermost: the CTAs of a wave share one head's keys in L2; long items first
     const int tail = max(0, int(blockIdx.x) - a.whole);
@@ -204,6 +210,24 @@ __device__ __forceinline__ bool find_work(const PagedPrefillArgs& a, int cap, in
     return false;
   }
   most = __reduce_max_sync(kFull, most);
+  if (ways == 2) {
+    // items of one half, whose CTAs' halves take the steps in turn, where there are CTAs for them
+    int all = 0, near = 0;
+#pragma unroll
+    for (int i = 0; i < 3; ++i) {
+      all += units[i] ? (n[i] + half_tokens - 1) / half_tokens * a.H_kv : 0;
+      near += units[i] * min(steps[i], kNear + 1);
+    }
+    if (__reduce_add_sync(kFull, all) <= int(gridDim.x) && __reduce_add_sync(kFull, near) <= kNear) {
+      w.per = per = half_tokens;
+#pragma unroll
+      for (int i = 0; i < 3; ++i) {
+        if (!units[i]) continue;
+        units[i] = (n[i] + per - 1) / per * a.H_kv;
+        steps[i] = request_steps(a, L[i], n[i], per, cap);
+      }
+    }
+  }
   int lo = kMinPart, hi = max(kMinPart, most);
   while (lo < hi) {
     const int mid = (lo + hi) >> 1;
@@ -252,12 +276,12 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
   uint8_t* ring = smem + C::kQBytes;
   Shared& sh = *reinterpret_cast<Shared*>(smem + C::kSharedAt);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int G = a.G, pss = a.ps_shift, half_tokens = 128 / G, item_tokens = C::kWays * half_tokens;
+  const int G = a.G, pss = a.ps_shift, half_tokens = 128 / G;
   const int cap = int(min(int64_t(a.bt_stride) << pss, int64_t(0x7fffffff)));
 
   if (warp == 0) {
     Work w;
-    const bool any = find_work(a, cap, item_tokens, w);
+    const bool any = find_work(a, cap, half_tokens, C::kWays, w);
     if (any && w.item == 0 && w.h == 0 && w.part == 0 && lane == 0) {
       if (w.c0 < 0 || int64_t(w.c0) + w.n > a.T || w.L < w.n) flag(a.status, SA_DEV_BAD_COUNT);
       if (w.L > cap) flag(a.status, SA_DEV_OVERFLOW);
@@ -302,7 +326,7 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
     if (warp == C::kMmaWarp) tc5_dealloc(tmem, C::kCols);
     return;
   }
-  const int h = w.h, t0 = w.item * item_tokens, nt = min(item_tokens, w.n - t0);
+  const int h = w.h, t0 = w.item * w.per, nt = min(w.per, w.n - t0);
   const int first = w.L - w.n + t0, last = first + nt - 1, len = min(max(w.L, 0), cap);
   const Span<kKeys> sp(first, last, len, a.window, a.n_sink);
   const int per = (sp.tiles + w.parts - 1) / w.parts;

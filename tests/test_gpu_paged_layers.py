@@ -370,6 +370,18 @@ def test_prefill_items_behind_the_last_full_round(D, window):
     _prefill(Problem([700, 4500, 40], Hkv=8, G=16, D=D), [40, 290, 1], window=window, ws=ws)
 
 
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_of_few_rows_in_halves_and_whole(D):
+    # 1 - 3 halves of rows over few keys (items of one half) and over many (items of two)
+    for L in (900, 40_000):
+        p = Problem([L, 700], Hkv=8, G=8, D=D)
+        for new in ([15, 1], [30, 40], [16, 33]):
+            q, out, lse, ws = _prefill(p, new)
+            _prefill(p, new, window=600, n_sink=4, q=q, ws=ws)
+            again = _prefill(p, new, q=q, ws=ws)
+            assert torch.equal(again[1], out) and torch.equal(again[2], lse)
+
+
 def test_prefill_of_more_items_than_run_at_once():
     _prefill(Problem([3000, 33, 0, 1200], Hkv=8, G=7, D=64, ps=32), [2999, 30, 0, 5])
     _prefill(Problem([1900, 700], Hkv=8, G=5, D=64, ps=4), [1500, 700], window=333, n_sink=2)
