@@ -89,10 +89,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   auto length = [&](int b) { return max(0, a.seq_lens[b]); };
   auto span = [&](int L) { return Span<16>(L - 1, L - 1, min(L, cap), a.window, a.n_sink); };
 
-  if (kTma && threadIdx.x == 0) {
-    for (int w = 0; w < kWarps; ++w)
-      for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&s_bar[w][s]), 1);
-    mbar_init_fence();
+  // A warp's barriers are its own: its first lane makes them, and the warp meets before any lane arms or waits on one
+  // (no barrier of the block stands between this and a warp's first copies).
+  if constexpr (kTma) {
+    if (lane == 0) {
+      for (int s = 0; s < kStages; ++s) mbar_init(smem_u32(&s_bar[warp][s]), 1);
+      mbar_init_fence();
+    }
+    __syncwarp();
   }
   // Groups of a request (an empty one has a group per head too: its outputs are written). Every warp finds its
   // places by itself, 32 requests at a time.
