@@ -653,7 +653,9 @@ sa_status sa_append_kv_rope(const sa_cache* cache, const sa_batch* batch, const 
 
 /* Bytes of workspace sa_paged_decode needs (host function; reads the device's SM count). The workspace is
  * zero-filled once before its first use (sa_decode_workspace_init does this); every call leaves its counters
- * at zero again. Calls, and captured graphs, that share a workspace must be ordered on one stream. */
+ * at zero again, at a place that does not depend on its sizes. So one workspace, of the most bytes that any
+ * of them needs, serves calls of all sizes, of sa_paged_decode and of sa_paged_prefill; calls, and captured
+ * graphs, that share it must be ordered on one stream. */
 size_t sa_paged_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim);
 
 /*

@@ -4,6 +4,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "host.h"
 
 namespace sa {
 
@@ -27,6 +28,13 @@ struct Span {
   }
   __device__ __forceinline__ int start(int t) const { return (t < sink_tiles ? t : t - sink_tiles + win_tile) * R; }
 };
+
+// A workspace of either call begins with the counters of units that are cut into parts, one for each CTA that runs at
+// once: a region of the same size whatever the call's, so that no partial result of one call lies where another call,
+// or the other operator, counts.
+constexpr int kTicketsPerSm = 2;
+inline size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
+inline size_t ticket_bytes() { return align256(size_t(kTicketsPerSm) * sm_count() * sizeof(int32_t)); }
 
 // One more part of a unit is in memory: parts counted before it. Called by one
 // thread after the block's barrier; publishes the block's writes, and makes the

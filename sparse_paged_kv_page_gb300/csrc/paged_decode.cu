@@ -48,7 +48,7 @@ struct PagedDecodeArgs {
   float* lse;
   float* part_o;        // [CTAs][2][G][D]
   float* part_lse;      // [CTAs][2][G]
-  int32_t* tickets;     // [batch * H_kv]
+  int32_t* tickets;     // [CTAs]: of the cut unit that begins in a CTA
   int32_t* status;
   int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, window, n_sink;
   float scale_log2;
@@ -319,8 +319,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
       const int c_last = int(((int64_t(d_unit_at) + d_groups) * N - 1) / total);
       const int parts = c_last - c_first + 1;
       __syncthreads();
-      const int unit = d_b * a.H_kv + d_h;
-      if (threadIdx.x == 0) s_last = ticket(&a.tickets[unit]) == parts - 1;
+      // of the units that begin in a CTA the last alone is cut
+      if (threadIdx.x == 0) s_last = ticket(&a.tickets[c_first]) == parts - 1;
       __syncthreads();
       if (s_last) {
         // A thread merges four columns of a row, kFlight parts in flight, in the order of the parts; where the rows
@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
             if (a.lse && idx % D == 0) a.lse[row0 + row] = tot != 0.f ? M + lg2_approx(tot) * kLn2 : -INFINITY;
           }
         }
-        if (threadIdx.x == 0) a.tickets[unit] = 0;
+        if (threadIdx.x == 0) a.tickets[c_first] = 0;
       }
     }
     __syncthreads();                                     // the merge area is free again
@@ -503,14 +503,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm)
   if constexpr (!kTma) cp_async_wait<0>();
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 struct WsLayout {
   size_t part_lse, part_o, total;
 };
-WsLayout ws_layout(int batch, int H_kv, int G, int D, int ctas) {
+WsLayout ws_layout(int G, int D, int ctas) {
+  static_assert(kCtasPerSm <= kTicketsPerSm, "a counter for each CTA");
   WsLayout w;
-  w.part_lse = align256(size_t(batch) * H_kv * 4);
+  w.part_lse = ticket_bytes();
   w.part_o = w.part_lse + align256(size_t(ctas) * 2 * G * 4);
   w.total = w.part_o + size_t(ctas) * 2 * G * D * 4;
   return w;
@@ -542,7 +541,7 @@ extern "C" size_t sa_paged_decode_workspace_size(int32_t batch, int32_t num_kv_h
                                                  int32_t head_dim) {
   using namespace sa;
   if (batch <= 0 || num_kv_heads <= 0 || num_q_heads <= 0 || head_dim <= 0 || num_q_heads % num_kv_heads) return 0;
-  return ws_layout(batch, num_kv_heads, num_q_heads / num_kv_heads, head_dim, kCtasPerSm * sm_count()).total;
+  return ws_layout(num_q_heads / num_kv_heads, head_dim, kCtasPerSm * sm_count()).total;
 }
 
 extern "C" sa_status sa_paged_decode(const sa_cache* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
@@ -563,7 +562,7 @@ extern "C" sa_status sa_paged_decode(const sa_cache* cache, const sa_batch* batc
   if (cap > 0x7fffffff || most > 0x3fffffff) return SA_ERR_UNSUPPORTED;
   const int sms = kCtasPerSm * sm_count();
   const int ctas = most < sms ? int(most) : sms;
-  const WsLayout w = ws_layout(batch->batch, H, G, D, sms);
+  const WsLayout w = ws_layout(G, D, sms);
   if (!workspace || workspace_bytes < w.total || !aligned16(workspace)) return SA_ERR_WORKSPACE;
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   PagedDecodeArgs a = {};

@@ -66,7 +66,7 @@ struct PagedPrefillArgs {
   float* lse;
   float4* part_o;       // [CTAs][D / 4][rows]: a warp stores adjacent rows
   float* part_lse;      // [CTAs][rows]
-  int32_t* tickets;     // [units]
+  int32_t* tickets;     // [units that can be cut], no more than CTAs run at once
   int32_t* status;
   int H_kv, H_q, G, ps_shift, num_blocks, bt_stride, batch, T, window, n_sink, items, split;
   int whole, tail_parts;  // without split: CTAs before the last units, and parts of each of those
@@ -913,8 +913,6 @@ __global__ void __launch_bounds__(Cfg<D, kTma>::kThreads, 3 - ways(D))
   if (threadIdx.x == 0) a.tickets[w.unit] = 0;
 }
 
-size_t align256(size_t x) { return (x + 255) & ~size_t(255); }
-
 // Items of a call: at most one partly filled one per request.
 int64_t items_of(int64_t tokens, int batch, int G, int D) { return tokens / (ways(D) * (128 / G)) + batch; }
 
@@ -923,14 +921,16 @@ int64_t items_of(int64_t tokens, int batch, int G, int D) { return tokens / (way
 bool splits(int64_t units, int batch, int ctas) { return 2 * units <= ctas && batch <= 96; }
 
 // CTAs that run at once.
-int resident(int D) { return sm_count() * (3 - ways(D)); }
+constexpr int per_sm(int D) { return 3 - ways(D); }
+int resident(int D) { return sm_count() * per_sm(D); }
 
 struct WsLayout {
   size_t part_lse, part_o, total;
 };
 WsLayout ws_layout(int64_t ctas, int D) {
+  static_assert(per_sm(64) <= kTicketsPerSm && per_sm(128) <= kTicketsPerSm, "a counter for each CTA");
   WsLayout w;
-  w.part_lse = align256(size_t(ctas) * 4);
+  w.part_lse = ticket_bytes();
   w.part_o = w.part_lse + size_t(ctas) * 128 * ways(D) * 4;
   w.total = w.part_o + size_t(ctas) * 128 * ways(D) * D * 4;
   return w;

@@ -35,3 +35,53 @@ def test_decode_after_other_kernels_has_its_first_copies(D):
                 check_attention(got[0][b:b + 1], got[1][b:b + 1],
                                 attention64(q[b:b + 1], *p.seqs[b], torch.tensor([L - 1], device="cuda"), D ** -0.5, 0, 0))
         assert int(p.status) == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
+def _prefill_once(p, q, new, ws, **kw):
+    out = torch.full_like(q, float("nan"))
+    lse = torch.full(q.shape[:2], float("nan"), device="cuda")
+    cu = torch.tensor([0] + list(new), dtype=torch.int32).cumsum(0).to(torch.int32).cuda()
+    p.S.sa_paged_prefill(p.cache, p.batch, q, p.Hq, cu, 0.0, out, lse=lse, workspace=ws, dev_status=p.status, **kw)
+    return out, lse
+
+
+def test_one_workspace_serves_calls_of_all_sizes():
+    """Allocated once for the largest, as a server does: small batches, large ones, other heads, both operators in turn,
+    each against float64 and the same bits again in a workspace of its own."""
+    import sparse_paged_kv_page_gb300 as S
+    kinds = [dict(lens=[3000], Hkv=8, G=4), dict(lens=[1500 + 40 * i for i in range(16)], Hkv=8, G=4),
+             dict(lens=[9000, 70, 800], Hkv=3, G=7, D=64), dict(lens=[50] * 63 + [4000], Hkv=8, G=8),
+             dict(lens=[2000, 1], Hkv=1, G=16, dtype="fp16", ps=4), dict(lens=[5000], Hkv=8, G=16, D=64)]
+    calls = []
+    for seed, kw in enumerate(kinds):
+        p = Problem(kw.pop("lens"), seed=seed, **kw)
+        few = [min(n, 1 + b % 3) for b, n in enumerate(p.lens)]
+        qd, qp = p.rand(p.B, p.Hq, p.D), p.rand(sum(few), p.Hq, p.D)
+        calls += [(p, lambda ws, p=p, q=qd: _decode_once(p, q, ws), qd, [1] * p.B),
+                  (p, lambda ws, p=p, q=qp, n=few: _prefill_once(p, q, n, ws), qp, few)]
+    # whole items and, behind the last full round of CTAs, items in parts
+    for seed, D in ((20, 128), (21, 64)):
+        p = Problem([5000], Hkv=8, G=16, D=D, seed=seed)
+        q = p.rand(320, p.Hq, D)
+        calls.append((p, lambda ws, p=p, q=q: _prefill_once(p, q, [320], ws), q, [320]))
+    size = max(max(S.sa_paged_decode_workspace_size(p.B, p.H, p.Hq, p.D),
+                   S.sa_paged_prefill_workspace_size(p.B, p.H, p.Hq, p.D, q.shape[0])) for p, _, q, _ in calls)
+    shared = torch.zeros(size, dtype=torch.uint8, device="cuda")
+    order = list(range(len(calls))) + [len(calls) - 1 - i for i in range(len(calls))] + [2, 0, 6, 2, 7, 1, 12, 3, 13, 0, 6, 11, 2]
+    wanted = {}
+    for i in order:
+        p, call, q, new = calls[i]
+        out, lse = call(shared)
+        torch.cuda.synchronize()
+        assert int(p.status) == 0
+        if i not in wanted:
+            wanted[i] = out, lse
+            at = 0
+            for b, (L, n) in enumerate(zip(p.lens, new)):
+                r = slice(at, at + n)
+                check_attention(out[r], lse[r], attention64(q[r], *p.seqs[b], torch.arange(L - n, L, device="cuda"),
+                                                            p.D ** -0.5, 0, 0))
+                at += n
+            alone = call(torch.zeros(size, dtype=torch.uint8, device="cuda"))
+            assert torch.equal(alone[0], out) and torch.equal(alone[1], lse)
+        assert torch.equal(out, wanted[i][0]) and torch.equal(lse, wanted[i][1]), f"call {i} changed"
