@@ -23,3 +23,41 @@ def test_barriers_are_made_before_any_warp_uses_them(name):
         assert met.startswith("__sync"), f"{met} before the threads have met"
         if met == "__syncwarp()":
             assert "[warp]" in src[begin:made.start()], "a warp met, but the barriers are not its own"
+
+
+FIRST_CALLS = r"""
+#include <chrono>
+#include <cstdio>
+#include <thread>
+
+#include "tma_map.h"
+
+// A lookup that takes its time, in place of the runtime's.
+extern "C" cudaError_t CUDARTAPI cudaGetDriverEntryPointByVersion(const char*, void** p, unsigned int, unsigned long long,
+                                                                  cudaDriverEntryPointQueryResult* q) {
+  std::this_thread::sleep_for(std::chrono::milliseconds(300));
+  *p = reinterpret_cast<void*>(0x1000);
+  *q = cudaDriverEntryPointSuccess;
+  return cudaSuccess;
+}
+
+int main() {
+  sa::EncodeFn seen[2];
+  std::thread first([&] { seen[0] = sa::encode_fn(); });
+  std::this_thread::sleep_for(std::chrono::milliseconds(100));
+  std::thread second([&] { seen[1] = sa::encode_fn(); });
+  first.join();
+  second.join();
+  std::printf("%d%d\n", seen[0] != nullptr, seen[1] != nullptr);
+}
+"""
+
+
+def test_first_calls_from_two_threads_both_find_the_tensor_map_encoder(tmp_path):
+    import subprocess
+    from sparse_paged_kv_page_gb300 import build as B
+    src, exe = tmp_path / "first_calls.cpp", tmp_path / "first_calls"
+    src.write_text(FIRST_CALLS)
+    subprocess.run([B._nvcc(), "-std=c++17", "-cudart", "none", "-I", B.CSRC, "-I", B.INCLUDE, str(src), "-o", str(exe),
+                    "-lpthread"], check=True)
+    assert subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout.strip() == "11"
