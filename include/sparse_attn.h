@@ -144,7 +144,8 @@ typedef struct sa_batch {
  * Written if cache->meta != NULL.
  *   new_cu            [batch + 1] int32, device, non-decreasing, new_cu[0] = 0
  *   max_new_per_req   host: an upper bound on any n_b (sizes the grid); n_b above
- *                     it sets SA_DEV_OVERFLOW and the excess is dropped
+ *                     it sets SA_DEV_OVERFLOW and the excess is dropped; 0: nothing
+ *                     is done, and k_new and v_new may be NULL
  *   hh                nullable bf16 [num_blocks * page_size, num_kv_heads]: the
  *                     H2O score of token slot (block * page_size + slot); the
  *                     slots written here are set to 0
@@ -631,7 +632,8 @@ typedef struct sa_rope {
  *   q         nullable (with q_out): keys and values alone
  *   num_q_heads  any count (not only a multiple of num_kv_heads)
  *   new_cu, max_new_per_req  as sa_append_kv; new_cu[batch] <= num_tokens, and
- *             rows from there on are padding: neither read nor written
+ *             rows from there on are padding: never used, never written. With
+ *             num_tokens 0 nothing is done, and the rows (and positions) may be NULL
  *   advanced  0: the new tokens follow the seq_lens[b] cached ones, and
  *             seq_lens[b] += n_b at the end; otherwise seq_lens already counts
  *             them (as for sa_h2o_prefill) and is left alone, so that the layers
@@ -694,7 +696,8 @@ size_t sa_paged_prefill_workspace_size(int32_t batch, int32_t num_kv_heads, int3
  * at its position sees. Prompts, chunks of prompts and a few drafted tokens.
  *   q, out   [num_tokens, num_q_heads, head_dim], dtype; 16-byte aligned; out
  *            may be q itself; rows from new_cu[batch] on are padding: never
- *            used, never written
+ *            used, never written; with num_tokens 0 nothing is done, and both
+ *            may be NULL
  *   new_cu   [batch + 1] int32, device, non-decreasing, new_cu[0] = 0
  *   lse      nullable float32 [num_tokens, num_q_heads], natural log
  * A request whose rows leave [0, num_tokens] sets SA_DEV_BAD_COUNT and is

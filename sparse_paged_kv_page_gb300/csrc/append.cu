@@ -259,7 +259,8 @@ sa_status sa::append_impl(const sa_cache* cache, const sa_batch* batch, const vo
   sa_status st = check_cache(cache, true, false);
   if (st != SA_OK) return st;
   if ((st = check_batch(batch)) != SA_OK) return st;
-  if (!k_new || !v_new || !new_cu || max_new_per_req < 0) return SA_ERR_INVALID_ARG;
+  if (!new_cu || max_new_per_req < 0) return SA_ERR_INVALID_ARG;
+  if (max_new_per_req > 0 && (!k_new || !v_new)) return SA_ERR_INVALID_ARG;   // (no rows: they may have no address)
   if ((ret_pos == nullptr) != (ret_cnt == nullptr)) return SA_ERR_INVALID_ARG;
   if (ret_pos && ret_cap <= 0) return SA_ERR_INVALID_ARG;
   if (max_new_per_req == 0) return SA_OK;

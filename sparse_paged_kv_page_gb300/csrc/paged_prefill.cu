@@ -979,7 +979,7 @@ extern "C" sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* bat
   sa_status st = check_cache(cache, true, false);
   if (st != SA_OK) return st;
   if ((st = check_batch(batch)) != SA_OK) return st;
-  if (!q || !out || !new_cu || num_tokens < 0 || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads)
+  if (!new_cu || num_tokens < 0 || (num_tokens > 0 && (!q || !out)) || num_q_heads <= 0 || num_q_heads % cache->num_kv_heads)
     return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || window < 0 || n_sink < 0) return SA_ERR_INVALID_ARG;
   const int G = num_q_heads / cache->num_kv_heads, D = cache->head_dim, H = cache->num_kv_heads;

@@ -613,14 +613,15 @@ extern "C" sa_status sa_append_kv_rope(const sa_cache* cache, const sa_batch* ba
   sa_status st = check_cache(cache, true, false);
   if (st != SA_OK) return st;
   if ((st = check_batch(batch)) != SA_OK) return st;
-  if (!rope || !k_new || !v_new || !new_cu || num_tokens < 0 || max_new_per_req < 0) return SA_ERR_INVALID_ARG;
+  if (!rope || !new_cu || num_tokens < 0 || max_new_per_req < 0) return SA_ERR_INVALID_ARG;
+  if (num_tokens > 0 && (!k_new || !v_new)) return SA_ERR_INVALID_ARG;   // (no rows: they may have no address)
   if ((q == nullptr) != (q_out == nullptr) || (q && num_q_heads <= 0)) return SA_ERR_INVALID_ARG;
   if ((ret_pos == nullptr) != (ret_cnt == nullptr) || (ret_pos && ret_cap <= 0)) return SA_ERR_INVALID_ARG;
   if (cache->kstd && !cache->meta) return SA_ERR_INVALID_ARG;
   const int D = cache->head_dim, H = cache->num_kv_heads;
   if (rope->rot_dim < 0 || rope->rot_dim > D || rope->rot_dim % 16) return SA_ERR_INVALID_ARG;
   if (rope->rot_dim && (!rope->table || rope->max_pos <= 0)) return SA_ERR_INVALID_ARG;
-  if (rope->num_axes < 1 || rope->num_axes > 4 || (rope->num_axes > 1 && !rope->positions)) return SA_ERR_INVALID_ARG;
+  if (rope->num_axes < 1 || rope->num_axes > 4 || (rope->num_axes > 1 && num_tokens > 0 && !rope->positions)) return SA_ERR_INVALID_ARG;
   if (!(rope->eps >= 0.f)) return SA_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(q_out) || !aligned16(rope->table) ||
       !aligned16(rope->q_weight) || !aligned16(rope->k_weight))

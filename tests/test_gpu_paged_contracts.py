@@ -85,3 +85,27 @@ def test_one_workspace_serves_calls_of_all_sizes():
             alone = call(torch.zeros(size, dtype=torch.uint8, device="cuda"))
             assert torch.equal(alone[0], out) and torch.equal(alone[1], lse)
         assert torch.equal(out, wanted[i][0]) and torch.equal(lse, wanted[i][1]), f"call {i} changed"
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+def test_calls_without_tokens(rotated):
+    import sparse_paged_kv_page_gb300 as S
+    from sparse_paged_kv_page_gb300.step import SparseDecoder
+    rope = S.make_rope(S.rope_table(64, 128)) if rotated else None
+    dec = SparseDecoder(batch=2, num_q_heads=4, num_kv_heads=2, head_dim=128, page_size=16, num_blocks=8, bt_stride=4,
+                        dense=True, rope=rope)
+    dec.set_block_table(torch.arange(8).view(2, 4))
+    g = torch.Generator().manual_seed(3)
+    rand = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    dec.prefill(rand(9, 2, 128), rand(9, 2, 128), [5, 4])
+    k, v = dec.cache.k.clone(), dec.cache.v.clone()
+    none = lambda h: torch.empty((0, h, 128), dtype=torch.bfloat16, device="cuda")  # noqa: E731
+    out = dec.prefill_attend(none(4), none(2), none(2), [0, 0])
+    dec.prefill(none(2), none(2), [0, 0])
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    three = S.make_rope(S.rope_table(64, 128), sections=[32, 32], positions=torch.empty((2, 0), dtype=torch.int32, device="cuda"))
+    S.sa_append_kv_rope(dec.cache.struct, dec.batch, three, none(4), none(2), none(2), cu, 0, none(4))
+    torch.cuda.synchronize()
+    assert out.shape == (0, 4, 128) and dec.seq_lens.tolist() == [5, 4] and int(dec.dev_status) == 0
+    assert torch.equal(dec.cache.k.view(torch.int16), k.view(torch.int16))
+    assert torch.equal(dec.cache.v.view(torch.int16), v.view(torch.int16))

@@ -61,3 +61,33 @@ def test_first_calls_from_two_threads_both_find_the_tensor_map_encoder(tmp_path)
     subprocess.run([B._nvcc(), "-std=c++17", "-cudart", "none", "-I", B.CSRC, "-I", B.INCLUDE, str(src), "-o", str(exe),
                     "-lpthread"], check=True)
     assert subprocess.run([str(exe)], check=True, capture_output=True, text=True, timeout=60).stdout.strip() == "11"
+
+
+def test_calls_without_tokens_need_no_rows():
+    """An empty tensor has no address: where a call has no token, its rows may be null (nothing is launched)."""
+    import ctypes
+    from sparse_paged_kv_page_gb300 import _lib, build as B
+    B.build()
+    lib, P = _lib.load(), ctypes.c_void_p
+    c = _lib.SaCache(k=P(0x100000), v=P(0x200000), meta=P(0x300000), dtype=0, num_blocks=4, num_kv_heads=2, page_size=16,
+                     head_dim=128, kstd=None)
+    b = _lib.SaBatch(block_table=P(0x20000), seq_lens=P(0x10000), batch=1, bt_stride=4)
+    cu, ref = P(0x800000), ctypes.byref
+
+    def rope(axes=1):
+        sec = (_lib.c_i32 * 4)(*([64, 0] if axes == 1 else [32, 32]), 0, 0)
+        return _lib.SaRope(table=P(0x400000), positions=None, q_weight=None, k_weight=None, max_pos=64, rot_dim=128,
+                           interleaved=0, num_axes=axes, sections=sec, eps=1e-6)
+
+    def append(T, most, r=rope()):
+        return lib.sa_append_kv_rope(ref(c), ref(b), ref(r), None, 512, 4, None, 256, None, 256, cu, T, most, 0, None, None,
+                                     None, None, 0, None, None)
+
+    def prefill(T):
+        return lib.sa_paged_prefill(ref(c), ref(b), None, 4, cu, T, 0, 0, 0.0, None, None, P(0xa00000), 1 << 30, None, None)
+
+    assert append(0, 0) == 0 and append(0, 4) == 0 and append(0, 0, rope(2)) == 0
+    assert append(3, 3) == 1 and append(3, 3, rope(2)) == 1
+    assert prefill(0) == 0 and prefill(3) == 1
+    plain = lambda most: lib.sa_append_kv(ref(c), ref(b), None, None, cu, most, None, None, None, 0, None, None)  # noqa: E731
+    assert plain(0) == 0 and plain(3) == 1
