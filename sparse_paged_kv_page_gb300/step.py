@@ -159,20 +159,22 @@ class SparseDecoder:
         key-as-query absorb and eviction instead of all at once. With a rotation
         (the decoder's, or `rope` for these tokens) k is normed and turned."""
         new_cu, mx = self._offsets(lens)
-        rope = rope or self.rope
-        if self.proxy_prefill:
-            if rope is not None:
-                sa_append_kv_rope(self.cache.struct, self.batch, rope, None, k, v, new_cu, mx, None,
-                                  hh=self.cache.hh, dev_status=self.dev_status)
-            else:
-                sa_append_kv(self.cache.struct, self.batch, k, v, new_cu, mx, hh=self.cache.hh,
-                             dev_status=self.dev_status)
-            sa_h2o_prefill(self.cache.struct, self.batch, new_cu, self.cache.hh,
-                           self.cache.hh.shape[0], self.ret_pos, self.ret_cnt, self.ret_cap,
-                           self.budget, self.n_sink, self.grace, self.decay, self.scale,
-                           dev_status=self.dev_status)
+        self._append_prompt(k, v, new_cu, mx, rope or self.rope)
+
+    def _append_prompt(self, k, v, new_cu, mx, rope, q=None, q_out=None):
+        """The append of prefill and prefill_attend; q is normed and turned into q_out where there is a rotation."""
+        if not self.proxy_prefill:
+            return self._append(k, v, new_cu, mx, rope=rope, q=q, q_out=q_out)
+        if rope is not None:
+            sa_append_kv_rope(self.cache.struct, self.batch, rope, q, k, v, new_cu, mx, q_out,
+                              hh=self.cache.hh, dev_status=self.dev_status)
         else:
-            self._append(k, v, new_cu, mx, rope=rope)
+            sa_append_kv(self.cache.struct, self.batch, k, v, new_cu, mx, hh=self.cache.hh,
+                         dev_status=self.dev_status)
+        sa_h2o_prefill(self.cache.struct, self.batch, new_cu, self.cache.hh,
+                       self.cache.hh.shape[0], self.ret_pos, self.ret_cnt, self.ret_cap,
+                       self.budget, self.n_sink, self.grace, self.decay, self.scale,
+                       dev_status=self.dev_status)
 
     def prefill_attend(self, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, lens: Sequence[int],
                        rope: Optional[SaRope] = None, out: Optional[torch.Tensor] = None,
@@ -180,17 +182,18 @@ class SparseDecoder:
         """Append lens[b] tokens per request and attend them: q [sum(lens), H_q, D], causal over the
         cache (with the decoder's window and first tokens when dense), into out (returned). With a
         rotation (the decoder's, or `rope` for these tokens) q and k are normed and turned first.
-        Every cached token is attended, whatever selection the decoder's steps use."""
+        Every cached token is attended, whatever selection the decoder's steps use; retained lists take
+        the tokens as in prefill."""
         new_cu, mx = self._offsets(lens)
         rope = rope or self.rope
         if out is None:
             out = torch.empty(q.shape, dtype=self.dtype, device=self.device)
         if rope is not None:
             q_rot = torch.empty(q.shape, dtype=self.dtype, device=self.device)
-            self._append(k, v, new_cu, mx, rope=rope, q=q, q_out=q_rot)
+            self._append_prompt(k, v, new_cu, mx, rope, q, q_rot)
             q = q_rot
         else:
-            self._append(k, v, new_cu, mx)
+            self._append_prompt(k, v, new_cu, mx, None)
         need = sa_paged_prefill_workspace_size(self.B, self.H_kv, self.H_q, self.D, q.shape[0])
         if self.prefill_ws is None or self.prefill_ws.numel() < need:
             self.prefill_ws = alloc_paged_prefill_workspace(self.B, self.H_kv, self.H_q, self.D, q.shape[0],

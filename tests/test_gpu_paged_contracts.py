@@ -109,3 +109,52 @@ def test_calls_without_tokens(rotated):
     assert out.shape == (0, 4, 128) and dec.seq_lens.tolist() == [5, 4] and int(dec.dev_status) == 0
     assert torch.equal(dec.cache.k.view(torch.int16), k.view(torch.int16))
     assert torch.equal(dec.cache.v.view(torch.int16), v.view(torch.int16))
+
+
+@pytest.mark.parametrize("rotated", [False, True])
+@pytest.mark.parametrize("proxy", [False, True])
+def test_attended_prompts_leave_the_lists_that_prompts_leave(proxy, rotated):
+    """Token-level decoders: prefill_attend retains, scores and evicts as prefill does, and the steps behind it agree."""
+    import sparse_paged_kv_page_gb300 as S
+    from sparse_paged_kv_page_gb300.step import SparseDecoder
+    B, Hkv, Hq, D, stride = 2, 2, 8, 64, 256
+    rope = S.make_rope(S.rope_table(stride, D)) if rotated else None
+    g = torch.Generator().manual_seed(11)
+    rand = lambda *s: torch.randn(s, generator=g).to(torch.bfloat16).cuda()  # noqa: E731
+    decs = []
+    for _ in range(2):
+        dec = SparseDecoder(batch=B, num_q_heads=Hq, num_kv_heads=Hkv, head_dim=D, page_size=1, num_blocks=B * stride,
+                            bt_stride=stride, budget=40, n_sink=4, grace=6, decay=0.95, ret_cap=48 if proxy else 200,
+                            proxy_prefill=proxy, rope=rope)
+        dec.set_block_table(torch.arange(B * stride).view(B, stride))
+        decs.append(dec)
+    seen, done = [[] for _ in range(B)], [0] * B
+    for lens in ([90, 30], [25, 60]):                     # the prompt is longer than the lists of the trimmed one
+        T = sum(lens)
+        q, k, v = rand(T, Hq, D), rand(T, Hkv, D), rand(T, Hkv, D)
+        decs[0].prefill(k, v, lens)
+        out = decs[1].prefill_attend(q, k, v, lens)
+        at = 0
+        for b, n in enumerate(lens):
+            done[b] += n
+            if not rotated:                               # every cached token is attended, whatever is retained
+                seen[b].append((k[at:at + n], v[at:at + n]))
+                kb, vb = (torch.cat(x) for x in zip(*seen[b]))
+                check_attention(out[at:at + n], None,
+                                attention64(q[at:at + n], kb, vb, torch.arange(done[b] - n, done[b], device="cuda"),
+                                            D ** -0.5, 0, 0))
+            at += n
+        torch.cuda.synchronize()
+        for name in ("seq_lens", "ret_cnt", "dev_status"):
+            assert torch.equal(getattr(decs[0], name), getattr(decs[1], name)), name
+        assert int(decs[1].dev_status) == 0
+        assert decs[1].ret_cnt.tolist() == [[40] * Hkv if proxy and n > 40 else [n] * Hkv for n in done]
+        for b in range(B):
+            for h in range(Hkv):
+                pos = [d.ret_pos[b, h, : int(d.ret_cnt[b, h])] for d in decs]
+                assert torch.equal(*pos)
+                hh = [d.cache.hh[d.block_table[b, x.long()].long(), h] for d, x in zip(decs, pos)]
+                assert torch.equal(*hh)
+    for _ in range(3):
+        q, k, v = rand(B, Hq, D), rand(B, Hkv, D), rand(B, Hkv, D)
+        assert torch.equal(*[d.step(q, k, v) for d in decs])
