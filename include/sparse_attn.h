@@ -248,8 +248,10 @@ sa_status sa_select_topk_reserved(const float* scores, int32_t max_pages, const 
  * these sizes (host function, no GPU access). The workspace holds the split
  * partial states and one ticket counter per (request, KV head); it must be
  * zero-filled once before its first use (sa_decode_workspace_init does this)
- * and every call leaves the counters at zero again. Calls that share a
- * workspace must be ordered on one stream.
+ * and every call leaves the counters at zero again. A call that merges by
+ * counters (splits that no cluster holds) clears its own first, so calls of
+ * other sizes may use the workspace in between. Calls that share a workspace
+ * must be ordered on one stream.
  */
 size_t sa_decode_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads,
                                 int32_t head_dim, int32_t page_size, int32_t sel_stride);

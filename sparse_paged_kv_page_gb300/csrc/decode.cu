@@ -679,7 +679,11 @@ sa_status launch_merge_mode(const DecodeArgs& a, dim3 grid, cudaStream_t s, cons
         launch_decode<T, D, kTma, true>(a, grid, s, mk, mv, g_dec_smem[4 * slot + 2 + kTma], pdl);
     if (st != SA_ERR_UNSUPPORTED) return st;
   }
-  if (a.nsplit > 1 && !a.tickets && !a.logits_only) return SA_ERR_WORKSPACE;
+  if (a.nsplit > 1 && !a.logits_only) {
+    if (!a.tickets) return SA_ERR_WORKSPACE;
+    // calls of other sizes may have kept partial results where this one counts
+    if (cudaMemsetAsync(a.tickets, 0, size_t(grid.y) * grid.z * sizeof(int32_t), s) != cudaSuccess) return SA_ERR_CUDA;
+  }
   return launch_decode<T, D, kTma, false>(a, grid, s, mk, mv, g_dec_smem[4 * slot + kTma], pdl);
 }
 
@@ -836,10 +840,6 @@ extern "C" sa_status sa_sparse_decode_noalloc(const sa_cache* cache, const sa_ba
     g_noalloc_addr[dev] = p;
   }
   void* ws = g_noalloc_addr[dev];
-  // the tickets must start at zero on every call (a call cut short could leave them set)
-  const size_t ticket_bytes = size_t(batch->batch) * cache->num_kv_heads * sizeof(int32_t);
-  if (cudaMemsetAsync(ws, 0, ticket_bytes, static_cast<cudaStream_t>(stream)) != cudaSuccess)
-    return SA_ERR_CUDA;
   return sa::decode_impl(cache, batch, q, num_q_heads, sel_idx, sel_cnt, sel_stride, scale, out, lse,
                          logits, logits_stride, ws, SA_NOALLOC_SCRATCH_BYTES, dev_status, stream,
                          /*allow_cluster=*/false, /*pdl=*/false, /*per_query_head=*/false,

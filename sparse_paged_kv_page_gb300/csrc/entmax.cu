@@ -771,6 +771,8 @@ sa_status launch_attend(const EntArgs& a, dim3 grid, cudaStream_t s, int* attr) 
         launch_ex(kc, grid, dim3(kThreads), size_t(smem), s, true, unsigned(a.nsplit), a) == cudaSuccess)
       return SA_OK;
     (void)cudaGetLastError();                              // refused: the ticket merge
+    // calls of other sizes may have kept their data where this one counts
+    if (cudaMemsetAsync(a.tickets, 0, size_t(grid.y) * grid.z * sizeof(int32_t), s) != cudaSuccess) return SA_ERR_CUDA;
   }
   auto kt = entmax_attend_kernel<T, D, kG, false>;
   if (!ensure_smem(kt, smem, attr)) return SA_ERR_CUDA;
@@ -831,8 +833,8 @@ sa_status entmax_impl(const sa_cache* cache, const sa_batch* batch, const void* 
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   float* lg = logits ? logits : reinterpret_cast<float*>(ws + w.logits);
   const int lg_stride = logits ? logits_stride : int(rows);
-  // the split counters start at zero (a zero-filled workspace); each call's
-  // last CTA per unit leaves its counter at zero again
+  // the split counters start at zero; each call's last CTA per unit leaves its
+  // counter at zero again
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   // (1) the logits of every selected token (K only)
   st = decode_impl(cache, batch, q, num_q_heads, sel_idx, sel_cnt, sel_stride, scale, out, nullptr, lg,
