@@ -158,3 +158,107 @@ def test_attended_prompts_leave_the_lists_that_prompts_leave(proxy, rotated):
     for _ in range(3):
         q, k, v = rand(B, Hq, D), rand(B, Hkv, D), rand(B, Hkv, D)
         assert torch.equal(*[d.step(q, k, v) for d in decs])
+
+
+# ---------------------------------------------------------------------------------------------- page means
+def _round_once(x, dtype):
+    """float64 rounded once to the type, to nearest even (a cast by way of float32 would round twice)."""
+    bits, least = (8, -133) if dtype is torch.bfloat16 else (11, -24)     # significant bits; exponent of the smallest step
+    _, e = torch.frexp(x)
+    step = torch.exp2((e.double() - bits).clamp(min=least))
+    return (torch.round(x / step) * step).to(dtype)
+
+
+def _columns(n, heads, D, dtype, g):
+    """Keys [n, heads, D] whose columns are, in turn: random; of mixed magnitude; cancelling; equal but for one step; on a
+    rounding border, or off it by a power of two. Their sums are exact in float64 in any order (44 bits)."""
+    k = torch.randn((n, heads, D), generator=g, dtype=torch.float64)
+    ulp = 2.0 ** -7 if dtype is torch.bfloat16 else 2.0 ** -10
+    low = -33 if dtype is torch.bfloat16 else -24
+    k[..., 1::8] *= torch.exp2(torch.randint(-9, 10, k[..., 1::8].shape, generator=g).double())
+    if n > 1:
+        k[n // 2: 2 * (n // 2), :, 2::8] = -k[: n // 2, :, 2::8].to(dtype).double()
+    k[..., 3::8] = 1.0
+    k[n // 3, :, 3::8] = 1.0 + ulp
+    if n >= 4 and n % 2 == 0:                             # the sum of all rows but the last is n (1 + ulp / 2)
+        for at in (4, 5, 6, 7):
+            k[..., at::8] = 1.0
+            k[0, :, at::8] = 2.0
+            k[1, :, at::8] = 1.0 + n / 2 * ulp
+            m = k[n - 1, :, at::8]
+            m[:] = torch.exp2(torch.randint(low, -8, m.shape, generator=g).double()) * (-1.0 if at & 1 else 1.0)
+            if at == 4:
+                m[:] = 0.0
+    return k.to(dtype)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("ps", [1, 2, 4, 8, 16, 32, 64, 128])
+def test_page_means_are_rounded_once(dtype, D, ps):
+    """min, max and mean of every page, exactly: whole pages, partly filled ones, pages completed by a second call; few
+    pages (a page's rows shared by warps) and many."""
+    import sparse_paged_kv_page_gb300 as S
+    H, g = 8, torch.Generator().manual_seed(ps + D)
+    rope = S.make_rope(None)                              # no rotation, no norm: the keys are stored as they come
+    for first, second in ((3 * ps + (ps + 1) // 2, 5 * ps), (0, 1500 * min(ps, 16) + 1)):
+        n = first + second
+        pages = -(-n // ps)
+        keys = torch.cat([_columns(min(ps, n - p * ps), H, D, dtype, g) for p in range(min(pages, 12))])
+        if pages > 12:                                    # the same twelve pages again and again
+            keys = torch.cat([keys.repeat(-(-pages // 12), 1, 1)[: n]])
+        keys = keys.cuda()
+        k = torch.full((pages, H, ps, D), float("nan"), dtype=dtype, device="cuda")
+        meta = torch.full((pages, H, 3, D), 7.0, dtype=dtype, device="cuda")
+        cache = S.make_cache(k, k.clone(), meta)
+        lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        table = torch.randperm(pages, generator=g).to(torch.int32).cuda()[None]
+        batch = S.make_batch(table, lens)
+        for part in (keys[:first], keys[first:]):
+            if part.shape[0]:
+                cu = torch.tensor([0, part.shape[0]], dtype=torch.int32, device="cuda")
+                S.sa_append_kv_rope(cache, batch, rope, None, part, part, cu, part.shape[0], None, dev_status=status)
+        torch.cuda.synchronize()
+        assert int(status) == 0 and lens.tolist() == [n]
+        got = meta[table[0].long()]                       # [pages, H, 3, D]
+        whole = n // ps
+        groups = [(got[:whole], keys[: whole * ps].view(whole, ps, H, D).transpose(1, 2))]
+        if n % ps:
+            groups.append((got[whole:], keys[whole * ps:].transpose(0, 1)[None]))
+        for m, rows in groups:
+            assert torch.equal(m[:, :, 0], rows.amin(2)) and torch.equal(m[:, :, 1], rows.amax(2))
+            want = _round_once(rows.double().sum(2) / rows.shape[2], dtype)
+            off = m[:, :, 2] != want
+            assert not bool(off.any()), f"{int(off.sum())} means, first at {off.nonzero()[0].tolist()}"
+
+
+@pytest.mark.parametrize("ps", [4, 16, 64, 128])
+@pytest.mark.parametrize("D", [64, 128])
+def test_page_statistics_of_wide_ranges_are_those_of_the_plain_append(D, ps):
+    """bf16 columns over all its exponents, with infinities and NaN: the same bits from both appends."""
+    import sparse_paged_kv_page_gb300 as S
+    H, n, g = 4, 5 * ps + ps // 2, torch.Generator().manual_seed(ps)
+    keys = torch.randn((n, H, D), generator=g, dtype=torch.float64)
+    keys *= torch.exp2(torch.randint(-130, 127, (n, 1, D), generator=g).double())
+    keys[:, 0] = torch.exp2(torch.randint(-133, 127, (1, D), generator=g).double()) * torch.randint(-3, 4, (n, D), generator=g)
+    keys[1, 1, 5::16], keys[2, 1, 6::16], keys[3, 2, 7::16] = float("inf"), -float("inf"), float("nan")
+    keys[4, 1, 5::32] = -float("inf")
+    keys = keys.to(torch.bfloat16).cuda()
+    pages, metas = -(-n // ps), []
+    table = torch.arange(pages, dtype=torch.int32, device="cuda")[None]
+    cu = torch.tensor([0, n], dtype=torch.int32, device="cuda")
+    for rotated in (False, True):
+        k = torch.zeros((pages, H, ps, D), dtype=torch.bfloat16, device="cuda")
+        meta = torch.full((pages, H, 3, D), 7.0, dtype=torch.bfloat16, device="cuda")
+        lens = torch.zeros(1, dtype=torch.int32, device="cuda")
+        cache, batch = S.make_cache(k, k.clone(), meta), S.make_batch(table, lens)
+        if rotated:
+            S.sa_append_kv_rope(cache, batch, S.make_rope(None), None, keys, keys, cu, n, None)
+        else:
+            S.sa_append_kv(cache, batch, keys, keys, cu, n)
+        metas.append(meta)
+    torch.cuda.synchronize()
+    a, b = metas
+    assert torch.equal(a.isnan(), b.isnan())
+    assert torch.equal(torch.where(a.isnan(), 0, a).view(torch.int16), torch.where(b.isnan(), 0, b).view(torch.int16))
