@@ -20,10 +20,10 @@
 // m16n8k16 (rows: the query heads, padded to 16), P rounded to the element type as
 // the operand, sums in float32.
 //
-// Measured: 4 requests of 131072 tokens, 64 / 8 heads of 128, 307 us, 7.0 TB/s (more than
-// a copy's 6.8: reads alone); 16 of 2048 - 32768, 174 us, 6.7 TB/s; pages of one token
-// behind a window of 4096, 79 us, bound by the rows' copies; one request of 1024, 7 us,
-// bound by the launch, three dependent loads and the merge.
+// Measured in replayed graphs: 4 requests of 131072 tokens, 64 / 8 heads of 128, 312 us,
+// 6.9 TB/s (more than a copy's 6.8: reads alone); 16 of 2048 - 32768, 178 us, 6.5 TB/s;
+// pages of one token behind a window of 4096, 81 us, bound by the rows' copies; one request
+// of 1024, 7.4 us, bound by the launch, three dependent loads and the merge.
 #include "common.cuh"
 #include "host.h"
 #include "paged.cuh"

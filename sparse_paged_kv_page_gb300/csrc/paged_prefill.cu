@@ -20,8 +20,10 @@
 // Value rows that no query of the CTA sees are zeroed in shared memory (a weight 0
 // times what a freed page holds must be 0), key rows masked.
 //
+// Times here and below are of the kernel in replayed graphs, where they vary by 2% with
+// the machine and its power; calls from Python of the two long prompts take 2 - 3% more.
 // Bound by the tensor cores for prompts (16384 tokens, 32 / 8 heads of 128, pages of 16:
-// 1310 us, 1.68 PFLOP/s; 2048 tokens behind 64000, 64 / 8 heads, 2510 us, 1.73 PFLOP/s:
+// 1315 us, 1.67 PFLOP/s; 2048 tokens behind 64000, 64 / 8 heads, 2540 us, 1.72 PFLOP/s:
 // the rate that the power limit leaves a dense product); at head dim 64 by
 // the rows' turn from S to P and the number of page copies (an operation costs about 80
 // cycles whatever its size: a prompt of 8192 over 4096 in pages of 16 1145 us, of 128

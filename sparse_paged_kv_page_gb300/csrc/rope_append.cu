@@ -38,7 +38,8 @@ constexpr int kQueryBatch = 2;                  // rows of queries a lane has in
 // Calls whose warps fit the SMs at once wait for loads: many rows in flight a lane,
 // three blocks an SM. Others need warps: five blocks an SM. Measured (us) as few / many:
 // 16 requests' single tokens with 2048 - 8192 cached 5.7 / 7.7, 4 x 8192 tokens 329 / 246
-// (1.37 GB: 82% of the measured copy bandwidth).
+// (1.37 GB: 82% of the measured copy bandwidth). Five blocks leave 96 registers a thread:
+// bf16 spills 4 or 5 words there, fp16 none.
 template <bool kFew>
 struct Depth {
   static constexpr int kBlocks = kFew ? 3 : 5;
