@@ -149,22 +149,19 @@ def _power(k):
     return ((k.to(torch.int32) + 127) << 23).view(torch.float32)
 
 
-def _quantise(x, dt):
+def _quantise(x):
     """Rows of float32 as e4m3 codes (bytes) and their scale 2 ** (byte - 127): the least power of two that brings the
-    row's largest magnitude to 448 at most, its exponent kept where every value held is exact in dt. A row that is not
-    finite has the byte 255 (NaN) and codes of 0."""
-    top = x.abs().amax(-1)
-    finite = top < math.inf
-    part, e = torch.frexp(top.masked_fill(~finite, 0))
-    low, high = (-15, 7) if dt == torch.float16 else (-64, 63)
-    k = torch.where(part > 0, e - 9 + (part > 0.875), low).clamp(low, high)
-    code = (x * _power(-k)[..., None]).clamp(-448, 448).masked_fill(~finite[..., None], 0).to(E4M3)
-    return code.view(torch.uint8), (k + 127).masked_fill(~finite, 255).to(torch.uint8)
+    row's largest finite magnitude to 448 at most, its exponent kept in [-64, 63]; what is not finite becomes NaN."""
+    finite = x.isfinite()
+    part, e = torch.frexp(x.abs().masked_fill(~finite, 0).amax(-1))
+    k = torch.where(part > 0, e - 9 + (part > 0.875), -64).clamp(-64, 63)
+    code = (x * _power(-k)[..., None]).clamp(-448, 448).masked_fill(~finite, math.nan).to(E4M3)
+    return code.view(torch.uint8), (k + 127).to(torch.uint8)
 
 
 def _values(code, scale):
     """What codes and scales (bytes) stand for, in float32."""
-    return code.view(E4M3).float() * _power(scale.to(torch.int32) - 127).masked_fill(scale == 255, math.nan)[..., None]
+    return code.view(E4M3).float() * _power(scale.to(torch.int32) - 127)[..., None]
 
 
 # -------------------------------------------------------------------------------------------------- inputs
@@ -186,7 +183,7 @@ def prepare(c, seed):
     for b in range(0, blocks, some):
         for x in range(2):
             rows = normal(*code[x][b:b + some].shape) + shared[x]
-            code[x][b:b + some], scale[b:b + some, :, x] = _quantise(rows, dt)
+            code[x][b:b + some], scale[b:b + some, :, x] = _quantise(rows)
     lens = torch.tensor(total, dtype=torch.int32, device="cuda")
     cu = torch.tensor([0] + [sum(new[: i + 1]) for i in range(B)], dtype=torch.int32, device="cuda")
     T = sum(new) if c["op"] not in ("decode", "sparse") else B
@@ -270,13 +267,13 @@ def _append_plain(s):
     place = first[b] + token - s["cu"].long()[b]
     block, slot = s["table"][b, place // ps].long(), place % ps
     k8, v8 = s["k"].view(torch.uint8), s["v"].view(torch.uint8)
-    k8[block, :, slot], s["scale"][block, :, 0, slot] = _quantise(k, dt)
-    v8[block, :, slot], s["scale"][block, :, 1, slot] = _quantise(s["v_new"].float(), dt)
+    k8[block, :, slot], s["scale"][block, :, 0, slot] = _quantise(k)
+    v8[block, :, slot], s["scale"][block, :, 1, slot] = _quantise(s["v_new"].float())
     # statistics of the pages written: the first and every token that opens a page stands for its page
     head = (slot == 0) | (token == s["cu"].long()[b])
     page, pb, blk = place[head] // ps, b[head], block[head]
     fill = (s["lens"].long()[pb] - page * ps).clamp(max=ps)
-    keys = _values(k8[blk], s["scale"][blk, :, 0])                              # [pages, Hkv, ps, D]
+    keys = _values(k8[blk], s["scale"][blk, :, 0]).to(dt).float()               # [pages, Hkv, ps, D], as they are read
     there = (torch.arange(ps, device=q.device) < fill[:, None])[:, None, :, None]
     s["meta"][blk, :, 0] = keys.masked_fill(~there, math.inf).amin(2).to(dt)
     s["meta"][blk, :, 1] = keys.masked_fill(~there, -math.inf).amax(2).to(dt)
@@ -391,11 +388,11 @@ def _turned(x, weight, place, c):
     return y
 
 
-def _rounded8(x, low, high):
+def _rounded8(x):
     """Rows of float64: the values of their e4m3 codes, on the format's grid, and their scales."""
     top = x.abs().amax(-1, keepdim=True)
-    scale = torch.exp2(torch.ceil(torch.log2(top.clamp(min=2.0 ** -60) / 448.0)).clamp(low, high))
-    scale = torch.where(top <= 224 * scale, (scale / 2).clamp(min=2.0 ** low), scale)           # a logarithm just above a whole number
+    scale = torch.exp2(torch.ceil(torch.log2(top.clamp(min=2.0 ** -60) / 448.0)).clamp(-64, 63))
+    scale = torch.where(top <= 224 * scale, (scale / 2).clamp(min=2.0 ** -64), scale)           # a logarithm just above a whole number
     y = x / scale
     quantum = torch.exp2(torch.floor(torch.log2(y.abs().clamp(min=2.0 ** -6))) - 3)             # 3 stored bits; fixed below 2 ** -6
     return (torch.round(y / quantum) * quantum).clamp(-448, 448), scale[..., 0]
@@ -413,8 +410,7 @@ def exact(c, seed):
     if c["op"] == "append":
         place = torch.cat([s["positions"][a:a + 1].t().expand(-1, w) for a, w in enumerate(_sections(c))], 1)
         q, k = _turned(s["q"], s["weights"][0], place, c), _turned(s["k_new"], s["weights"][1], place, c)
-        span = (-15, 7) if c["dtype"] == "fp16" else (-64, 63)
-        new_rows = [_rounded8(k, *span), _rounded8(s["v_new"].double(), *span)]
+        new_rows = [_rounded8(k), _rounded8(s["v_new"].double())]
         pools, meta = [s["k"].double(), s["v"].double()], s["meta"].double()
         scales = torch.exp2(s["scale"].double() - 127)
         row = 0
