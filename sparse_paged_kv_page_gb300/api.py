@@ -487,7 +487,7 @@ def _launch(fn_name: str, device: int, stream, *args):
 
 def _sizes(cache, kind):
     """Element type, device and sizes of a cache of that kind: dtype, device, blocks, KV heads, page size, head dim."""
-    if type(cache) is not kind:
+    if not isinstance(cache, kind):
         raise ValueError(f"cache must be a {kind.__name__}, got {type(cache).__name__}")
     pool = cache._keep[0]
     return (pool.dtype if kind is SaCache else cache._dtype, pool.get_device(), *pool.shape)
