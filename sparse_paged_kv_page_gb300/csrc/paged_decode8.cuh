@@ -817,7 +817,7 @@ __global__ void __launch_bounds__(32 * kMergeWarps) merge8_kernel(const __grid_c
 #pragma unroll
       for (int i = 0; i < kCols; ++i) acc[i] = 0.f;
       auto join = [&](float m, float t, const float (&x)[kCols]) {   // one more state: sums relative to e^m
-        if (m == -INFINITY) return;             // empty
+        if (m == -INFINITY && t == t) return;   // empty (states of NaN alone have no maximum, but a NaN sum)
         const float top = fmaxf(M, m), f = M == -INFINITY ? 0.f : ex2_approx((M - top) * kLog2e), w = ex2_approx((m - top) * kLog2e);
         tot = fmaf(t, w, tot * f);
         M = top;
