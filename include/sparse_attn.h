@@ -728,7 +728,9 @@ sa_status sa_paged_prefill(const sa_cache* cache, const sa_batch* batch, const v
  * c = x 2^-k rounded once to nearest even, beyond 448 to 448. Powers of two cost a
  * floating-point code no precision, and within these ranges every value held is
  * exact in dtype. A row that had a NaN or an infinity has s = 255 and is all NaN;
- * codes are never NaN themselves (0x7f, 0xff).
+ * codes are never NaN themselves (0x7f, 0xff). Rows that something else wrote keep
+ * to the same: scale bytes 63 .. 190 (bf16) or 112 .. 134 (fp16), or 255, and codes
+ * that are not NaN. What other bytes stand for differs from call to call.
  */
 typedef struct sa_cache8 {
   void* k;              /* [num_blocks, num_kv_heads, page_size, head_dim], e4m3 codes */

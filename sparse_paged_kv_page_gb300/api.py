@@ -613,7 +613,8 @@ def make_cache8(k: torch.Tensor, v: torch.Tensor, scale: torch.Tensor, meta: Opt
                 dtype=torch.bfloat16) -> SaCache8:
     """Struct view of pools of codes k, v float8_e4m3fn [num_blocks, H_kv, page_size, D], their scale bytes uint8
     [num_blocks, H_kv, 2, page_size] and (optional) meta [num_blocks, H_kv, 3, D] in dtype, the type of queries, new
-    rows and outputs. Its ``pages`` is the SaCache for the calls that read the statistics alone (sa_score_pages)."""
+    rows and outputs. Rows that are not sa_append_kv8's have scale bytes of 63 .. 190 (bfloat16), 112 .. 134 (float16) or
+    255, and no NaN codes. Its ``pages`` is the SaCache for the calls that read the statistics alone (sa_score_pages)."""
     if dtype not in _DT:
         raise ValueError("dtype must be bfloat16 or float16")
     if k.dtype != torch.float8_e4m3fn or v.dtype != k.dtype or k.shape != v.shape or k.dim() != 4:

@@ -1,8 +1,10 @@
-"""The calls over a cache held in 8 bits at what their documentation says beside the results: which rows a NaN reaches."""
+"""The calls over a cache held in 8 bits at what their documentation says beside the results: which rows a NaN reaches,
+which scale bytes a cache may hold."""
 import pytest
 import torch
 
-from kv8_util import Problem8
+from kv8_util import E4M3, Problem8, attention8, held64, quantise64
+from paged_util import check_attention
 
 pytestmark = pytest.mark.gpu
 
@@ -60,4 +62,54 @@ def test_prompts_a_nan_key_reaches_the_rows_that_see_it(T, D):
         nan = torch.zeros((T, 32), dtype=torch.bool, device="cuda")
         nan[max(0, token - (L - T)):, 16:] = True
         assert torch.equal(out.isnan().all(-1), nan) and torch.equal(out.isnan().any(-1), nan) and torch.equal(lse.isnan(), nan), token
+    assert int(p.status) == 0
+
+
+ENDS = {torch.bfloat16: (63, 190), torch.float16: (112, 134)}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("end", [0, 1])
+@pytest.mark.parametrize("D", [64, 128])
+def test_every_call_agrees_at_the_ends_of_the_scale_bytes(dtype, end, D):
+    """Keys and values whose scale bytes are the least or the largest that a cache of the type may hold: decode, lists of
+    pages, drafts, prompts from codes and on pages, and reading back all take the row as c 2^(byte - 127)."""
+    L, G = 3000, 16
+    p = Problem8([L], Hkv=1, G=G, D=D, dtype=dtype)
+    byte = ENDS[p.dt][end]
+    e = byte - 127
+    held, unit = [], []
+    for x in range(2):
+        code = quantise64(p.rand(L, 1, D).double(), p.dt)[0].float().to(E4M3)
+        p.put(0, 0, L, x, code, torch.full((L, 1), byte, dtype=torch.uint8, device="cuda"))
+        unit.append(code.double())
+        held.append(held64(code, torch.full((L, 1), byte, dtype=torch.uint8, device="cuda")))
+    scale = 2.0 ** -e / 2048
+
+    def check(out, lse, q, n, half_weights):
+        # the values in units of 2^e, so that the tolerance's absolute terms are those of numbers near 1
+        o, l, tol, tol_l = attention8(q, held[0], unit[1], torch.zeros_like(p.exps[0]), torch.arange(L - n, L, device="cuda"), scale,
+                                      0, 0, half_weights)
+        if p.dt == torch.float16:
+            tol = tol + 2.0 ** (-25 - e)                              # half a step of subnormal outputs
+        check_attention(out.double() * 2.0 ** -e, lse, (o, l, tol, tol_l))
+
+    S = p.S
+    q = p.rand(1, G, D)
+    out, lse = torch.empty_like(q), torch.empty((1, G), device="cuda")
+    ws = S.alloc_paged_decode8_workspace(1, 1, G, D)
+    S.sa_paged_decode8(p.cache, p.batch, q, G, scale, out, lse=lse, workspace=ws, dev_status=p.status)
+    check(out, lse, q, 1, True)
+    n = -(-L // 16)
+    sel = torch.arange(n, dtype=torch.int32, device="cuda").view(1, 1, n)
+    S.sa_sparse_decode8(p.cache, p.batch, q, G, sel, torch.full((1, 1), n, dtype=torch.int32, device="cuda"), n, scale, out, lse=lse,
+                        workspace=ws, dev_status=p.status)
+    check(out, lse, q, 1, True)
+    for T, few in ((1, True), (40, False), (2900, False)):            # by warps, from codes, on pages
+        q = p.rand(T, G, D)
+        check(*_prefill(p, q, [T], scale=scale), q, T, few)
+    rows = [torch.empty((L, 1, D), dtype=p.dt, device="cuda") for _ in range(2)]
+    S.sa_read_kv8(p.cache, p.batch, _offsets([L]), None, *rows, dev_status=p.status)
+    for x in range(2):
+        assert torch.equal(rows[x].double(), held[x])
     assert int(p.status) == 0
