@@ -801,8 +801,15 @@ size_t sa_paged_prefill8_workspace_size(int32_t batch, int32_t num_kv_heads, int
 /*
  * sa_paged_prefill8 -- sa_paged_prefill over a cache held in 8 bits that already
  * holds the new tokens (sa_append_kv8 first). The values held are turned into dtype,
- * which is exact, on the way to the tensor cores, or into the workspace before; where
- * requests have few rows, as in sa_paged_decode8. Everything else as sa_paged_prefill.
+ * which is exact, on the way to the tensor cores, or into the workspace before, and
+ * the weights are rounded to dtype. Calls whose requests have few rows (token, query
+ * head) of a KV head on the mean (num_tokens / batch * num_q_heads / num_kv_heads <= 32,
+ * or 16 where head_dim is 128 and batch * num_kv_heads < 16; batch <= 1024, and all
+ * tables together short enough for its counts) attend all of their requests as
+ * sa_paged_decode8 does, with weights to 2^-11: a request's last bits can so depend on
+ * the others of its call, and a long chunk beside many single tokens takes longer than
+ * in a call of its own. A request whose offsets decrease has no rows.
+ * Everything else as sa_paged_prefill.
  */
 sa_status sa_paged_prefill8(const sa_cache8* cache, const sa_batch* batch, const void* q, int32_t num_q_heads,
                             const int32_t* new_cu, int32_t num_tokens, int32_t window, int32_t n_sink, float scale,

@@ -1,5 +1,5 @@
 """The calls over a cache held in 8 bits at what their documentation says beside the results: which rows a NaN reaches,
-which scale bytes a cache may hold."""
+which scale bytes a cache may hold, what weights the rows of a call get, what is flagged, counters that are zero again."""
 import pytest
 import torch
 
@@ -113,3 +113,80 @@ def test_every_call_agrees_at_the_ends_of_the_scale_bytes(dtype, end, D):
     for x in range(2):
         assert torch.equal(rows[x].double(), held[x])
     assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("lens,new,kw", [
+    ([6000, 2500, 9], [3, 8, 1], dict(Hkv=2, G=4, D=64)), ([30_000], [2], dict(Hkv=1, G=8)),
+    ([5000, 700, 40, 1, 0, 33, 260, 9], [1, 15, 1, 1, 0, 1, 2, 0], dict(Hkv=3, G=4)),
+    ([5000, 700, 40, 1, 0, 33, 260, 9], [1, 7, 1, 1, 0, 1, 2, 0], dict(Hkv=3, G=8, D=64)),
+    ([2600] + [40 + 9 * i for i in range(63)], [70] + [1] * 63, dict(Hkv=2, G=4)),
+    ([2600] + [40 + 9 * i for i in range(63)], [190] + [1] * 63, dict(Hkv=2, G=8, D=64, ps=4))])
+def test_requests_of_few_rows_on_the_mean_get_16_bit_weights_of_11_bits(lens, new, kw):
+    """Calls of bfloat16 whose requests have few rows on the mean, and all of their requests, long ones too: weights are
+    rounded as in sa_paged_decode8 (2^-11), not to the element type."""
+    p = Problem8(lens, **kw)
+    assert sum(new) * p.G <= (32 if p.D == 64 or p.B * p.H >= 16 else 16) * p.B
+    for window, n_sink in ((0, 0), (300, 4)):
+        q = p.rand(sum(new), p.Hq, p.D, scale=2.0)
+        out, lse = _prefill(p, q, new, window=window, n_sink=n_sink)
+        cu = _offsets(new).tolist()
+        for b, L in enumerate(p.lens):
+            r = slice(cu[b], cu[b + 1])
+            want = attention8(q[r], *p.seqs[b], p.exps[b], torch.arange(L - new[b], L, device="cuda"), p.D ** -0.5, window, n_sink, True)
+            check_attention(out[r], lse[r], want)
+    assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_all_counters_of_a_workspace_are_zero_after_every_call(D):
+    """The counters are four for each SM of the device, whatever the call's size."""
+    counters = 4 * 4 * torch.cuda.get_device_properties(0).multi_processor_count
+    p = Problem8([40_000, 9, 2500, 0], Hkv=4, G=4, D=D)
+    S = p.S
+    for T, new in ((4, [1, 1, 1, 1]), (14, [5, 0, 9, 0]), (700, [300, 9, 391, 0]), (2500, [0, 0, 2500, 0])):
+        q = p.rand(T, p.Hq, D)
+        ws = S.alloc_paged_prefill8_workspace(p.B, p.H, p.Hq, D, T)
+        first, _ = _prefill(p, q, new if T > 4 else [1, 1, 1, 0], ws=ws)
+        assert not bool(ws[:counters].any())
+        again, _ = _prefill(p, q, new if T > 4 else [1, 1, 1, 0], ws=ws)
+        assert torch.equal(first, again) and not bool(ws[:counters].any())
+    ws = S.alloc_paged_decode8_workspace(p.B, p.H, p.Hq, D)
+    q = p.rand(p.B, p.Hq, D)
+    out = torch.empty_like(q)
+    S.sa_paged_decode8(p.cache, p.batch, q, p.Hq, 0.0, out, workspace=ws, dev_status=p.status)
+    assert not bool(ws[:counters].any())
+    n = 2500
+    sel = torch.arange(n, dtype=torch.int32, device="cuda").expand(p.B, p.H, n).contiguous()
+    cnt = torch.tensor([n, 1, 157, 0], dtype=torch.int32, device="cuda")[:, None].expand(p.B, p.H).contiguous()
+    S.sa_sparse_decode8(p.cache, p.batch, q, p.Hq, sel, cnt, n, 0.0, out, workspace=ws, dev_status=p.status)
+    assert not bool(ws[:counters].any()) and int(p.status) == 0
+
+
+def test_every_kind_of_bad_data_of_a_decode_is_flagged():
+    p = Problem8([100, 50, 20], Hkv=1, G=2)
+    q = p.rand(3, 2, 128)
+    ws, out = p.S.alloc_paged_decode8_workspace(3, 1, 2, 128), torch.empty_like(q)
+    for change, bit in ((lambda: None, 0), (lambda: p.table[0, 1].fill_(-5), 1), (lambda: p.seq_lens[1].fill_(100_000), 2),
+                        (lambda: p.seq_lens[2].fill_(-3), 4)):
+        change()
+        p.status.zero_()
+        p.S.sa_paged_decode8(p.cache, p.batch, q, 2, 0.0, out, workspace=ws, dev_status=p.status)
+        assert int(p.status) & 7 & ~(2 * bit - 1 if bit else 0) == 0 and (int(p.status) & bit) == bit
+    assert int(p.status) == 7
+
+
+@pytest.mark.parametrize("G,rows", [(4, 8), (4, 600)])
+def test_offsets_that_decrease_leave_their_request_without_rows(G, rows):
+    """By warps and by the tensor cores: a request whose offsets decrease has no rows, and the others theirs."""
+    p = Problem8([900, 900, 900], Hkv=1, G=G)
+    q = p.rand(rows, G, 128)
+    out, ws = torch.full_like(q, 3.0), p.S.alloc_paged_prefill8_workspace(3, 1, G, 128, rows)
+    n = rows - 4
+    cu = torch.tensor([0, n, n - 2, rows - 2], dtype=torch.int32).cuda()
+    p.S.sa_paged_prefill8(p.cache, p.batch, q, G, cu, 0.0, out, workspace=ws, dev_status=p.status)
+    assert int(p.status) == 0
+    want = attention8(q[:n - 2], *p.seqs[0], p.exps[0], torch.arange(900 - n, 898, device="cuda"), 128 ** -0.5, 0, 0, rows == 8)
+    check_attention(out[:n - 2], None, want)
+    want = attention8(q[n:n + 2], *p.seqs[2], p.exps[2], torch.arange(898, 900, device="cuda"), 128 ** -0.5, 0, 0, rows == 8)
+    check_attention(out[n:n + 2], None, want)
+    assert bool((out[n + 2:] == 3.0).all())
