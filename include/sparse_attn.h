@@ -791,10 +791,11 @@ sa_status sa_sparse_decode8(const sa_cache8* cache, const sa_batch* batch, const
                             void* out, float* lse, void* workspace, size_t workspace_bytes, int32_t* dev_status,
                             void* stream);
 
-/* Bytes of workspace sa_paged_prefill8 needs for num_tokens rows of q; rules as sa_paged_decode_workspace_size. For
- * many tokens it has room for 16-bit copies of as many cached ones (4 * num_kv_heads * head_dim bytes each), on which
- * calls run that find room for all of their requests' tokens there. More bytes are used: chunks of a prompt run faster
- * in a workspace of the size for the tokens that will be cached in the end. */
+/* Bytes of workspace for sa_paged_prefill8 of num_tokens rows of q; rules as sa_paged_decode_workspace_size, and one
+ * for the most requests and tokens serves calls of fewer. For many tokens it has room for 16-bit copies of as many
+ * cached ones (4 * num_kv_heads * head_dim bytes each), on which calls run that find room for all of their requests'
+ * tokens there; others run without. More bytes are used: chunks of a prompt run faster in a workspace of the size for
+ * the tokens that will be cached in the end. */
 size_t sa_paged_prefill8_workspace_size(int32_t batch, int32_t num_kv_heads, int32_t num_q_heads, int32_t head_dim,
                                         int32_t num_tokens);
 

@@ -1253,10 +1253,10 @@ sa_status prefill_call(const sa_cache* cache, const sa_cache8* cache8, const sa_
   if (G > 16) return SA_ERR_UNSUPPORTED;
   // pool rows are counted in 32 bits
   if (kQ8 && uint64_t(cache->num_blocks) * H * cache->page_size >= 0xffffffffull) return SA_ERR_UNSUPPORTED;
-  if (!workspace || !aligned16(workspace) ||
-      workspace_bytes < (kQ8 ? sa_paged_prefill8_workspace_size : sa_paged_prefill_workspace_size)(batch->batch, H, num_q_heads,
-                                                                                              D, num_tokens))
-    return SA_ERR_WORKSPACE;
+  // (over 8 bits room for pages is no need: a workspace for more requests may have none where fewer of as many tokens want it)
+  const size_t need = kQ8 ? few_workspace(num_tokens, batch->batch, G, D, H)
+                          : sa_paged_prefill_workspace_size(batch->batch, H, num_q_heads, D, num_tokens);
+  if (!workspace || !aligned16(workspace) || workspace_bytes < need) return SA_ERR_WORKSPACE;
   if (num_tokens == 0) return SA_OK;
   if (kQ8 && few_rows(num_tokens, G, D, H, batch->batch)) {
     const sa_status few = draft8_call(cache8, batch, q, num_q_heads, new_cu, num_tokens, window, n_sink, scale, out, lse,
@@ -1291,7 +1291,7 @@ sa_status prefill_call(const sa_cache* cache, const sa_cache8* cache8, const sa_
   a.part_o = reinterpret_cast<float4*>(ws + w.part_o);
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if constexpr (kQ8) {
-    st = laid_call(cache8, batch, q, a, workspace, workspace_bytes, few_workspace(num_tokens, batch->batch, G, D, H), s);
+    st = laid_call(cache8, batch, q, a, workspace, workspace_bytes, need, s);
     if (st != SA_OK) return st;
   }
   const bool bf = cache->dtype == SA_BF16;

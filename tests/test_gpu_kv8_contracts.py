@@ -190,3 +190,24 @@ def test_offsets_that_decrease_leave_their_request_without_rows(G, rows):
     want = attention8(q[n:n + 2], *p.seqs[2], p.exps[2], torch.arange(898, 900, device="cuda"), 128 ** -0.5, 0, 0, rows == 8)
     check_attention(out[n:n + 2], None, want)
     assert bool((out[n + 2:] == 3.0).all())
+
+
+@pytest.mark.parametrize("T,D", [(3000, 64), (6000, 128)])
+def test_a_workspace_for_more_requests_serves_fewer(T, D):
+    """The size for 64 requests has no room for 16-bit pages, which one request of as many tokens would like: it runs without."""
+    G = 16
+    p = Problem8([T], Hkv=1, G=G, D=D)
+    most, one = (p.S.sa_paged_prefill8_workspace_size(b, 1, G, D, T) for b in (64, 1))
+    assert most < one
+    ws = p.S.alloc_paged_prefill8_workspace(64, 1, G, D, T)
+    q = p.rand(T, G, D)
+    out, lse = _prefill(p, q, [T], ws=ws)
+    for r in (slice(0, 300), slice(T - 300, T)):
+        want = attention8(q[r], *p.seqs[0], p.exps[0], torch.arange(r.start, r.stop, device="cuda"), D ** -0.5, 0, 0, False)
+        check_attention(out[r], lse[r], want)
+    for T, new in ((2, [2]), (100, [100]), (1000, [1000])):
+        q = p.rand(T, G, D)
+        out, lse = _prefill(p, q, new, ws=ws)
+        want = attention8(q, *p.seqs[0], p.exps[0], torch.arange(p.lens[0] - T, p.lens[0], device="cuda"), D ** -0.5, 0, 0, T == 2)
+        check_attention(out, lse, want)
+    assert int(p.status) == 0
