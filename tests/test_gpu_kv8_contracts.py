@@ -211,3 +211,21 @@ def test_a_workspace_for_more_requests_serves_fewer(T, D):
         want = attention8(q, *p.seqs[0], p.exps[0], torch.arange(p.lens[0] - T, p.lens[0], device="cuda"), D ** -0.5, 0, 0, T == 2)
         check_attention(out, lse, want)
     assert int(p.status) == 0
+
+
+@pytest.mark.parametrize("kw,new", [
+    (dict(lens=[6000, 300, 9], Hkv=2, G=4), [5, 3, 1]), (dict(lens=[6000, 300, 9, 0], Hkv=4, G=7), [8, 3, 1, 0]),
+    (dict(lens=[3000], Hkv=2, G=16, D=64), [40]), (dict(lens=[9000, 2500], Hkv=8, G=4), [400, 300]),
+    (dict(lens=[6000], Hkv=1, G=16), [6000])])
+def test_prompts_and_drafts_into_their_queries(kw, new):
+    """out may be q itself: by warps, from codes, in parts and on pages the same bits as into rows of their own."""
+    lens = kw.pop("lens")
+    p = Problem8(lens, **kw)
+    q = p.rand(sum(new), p.Hq, p.D, scale=2.0)
+    out, lse = _prefill(p, q, new)
+    ws, lse2 = p.S.alloc_paged_prefill8_workspace(p.B, p.H, p.Hq, p.D, sum(new)), torch.empty_like(lse)
+    for _ in range(3):
+        x = q.clone()
+        p.S.sa_paged_prefill8(p.cache, p.batch, x, p.Hq, _offsets(new), 0.0, x, lse=lse2, workspace=ws, dev_status=p.status)
+        assert torch.equal(x, out) and torch.equal(lse, lse2)
+    assert int(p.status) == 0
