@@ -1202,7 +1202,9 @@ size_t few_workspace(int64_t tokens, int batch, int G, int D, int H) {
 // in registers go to the decode kernel, which turns no codes into values in shared memory; with 17 to 32 rows of 128 columns
 // only where there are units enough that each is cut into few parts. Measured (us) there / here, 32 query heads of 128 over 8
 // KV heads, four requests over 8000 - 30000: 1 - 2 tokens 44 / 78, 2 - 4 tokens 51 / 78, 3 - 8 tokens 64 / 77; one request over
-// 30000, 4 tokens 31 / 37, 8 tokens 43 / 37; heads of 64, 3 - 8 tokens of four 45 / 61, 8 of one 31 / 36.
+// 30000, 4 tokens 31 / 37, 8 tokens 43 / 37; heads of 64, 3 - 8 tokens of four 45 / 61, 8 of one 31 / 36. A mean does not see
+// a long request among short ones: 512 tokens behind 32000 beside 63 / 255 single tokens behind 1000 - 2000 take 529 / 1570
+// here, in a call of their own 234 and the single ones 54 / 154; 2048 tokens 975 / 1203 against 889 and 54 / 155.
 bool few_rows(int64_t tokens, int G, int D, int H, int batch) {
   const int most = D == 64 || batch * H >= 16 ? 32 : 16;
   return tokens * G <= most * int64_t(batch) && batch <= 1024;
@@ -1212,7 +1214,7 @@ bool few_rows(int64_t tokens, int G, int D, int H, int batch) {
 // those, and run on them; a CTA's own turning of its tiles slows its products by a fifth, at head dim 64 to half. Worth it
 // where that (`pairs`: of queries and keys that they see) takes longer than the pages do: their bytes, three for each code, and
 // 8 us of launches. Measured (us) there / here, 32 query heads over 8 KV heads: of 128, 16384 tokens 1560 / 1280, 4096 147 / 136,
-// 3000 94 / 107, eight prompts of 500 - 1200 106 / 109; of 64, 16384 tokens 2035 / 962, 2048 64 / 46, 1500 39 / 49, 2048 behind
+// 3000 94 / 107, eight prompts of 500 - 1200 106 / 109; of 64, 16384 tokens 2035 / 941, 2048 64 / 46, 1500 39 / 49, 2048 behind
 // 32000 1168 / 550; 2048 behind 64000 with 64 heads of 128 2970 / 2370.
 __host__ __device__ inline bool worth_pages(float pairs, float tokens, int Hq, int H, int D) {
   const float turning = (D == 128 ? 4.7e-10f : 2.6e-9f) * pairs * float(Hq * D), pages = 8.f + 1e-6f * tokens * float(H * D);

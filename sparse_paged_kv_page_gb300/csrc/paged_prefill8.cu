@@ -7,7 +7,7 @@
 // over HBM before (3 bytes read or written a code, here one page and head a block) does it once,
 // and the kernel over 16-bit pages then runs as it does for sa_paged_prefill, on pages of 128
 // whatever the cache's are: 16384 tokens, 32 / 8 heads of 128, 1270 - 1310 us, 1.68 - 1.73 PFLOP/s
-// (a CTA's own turning 1550; over a 16-bit cache with pages of 16, 1315 - 1330), heads of 64 962
+// (a CTA's own turning 1550; over a 16-bit cache with pages of 16, 1315 - 1330), heads of 64 941
 // (2035; 1161); a chunk of 2048 tokens x 64 heads behind 64000 in a workspace with room 2370
 // (2970; 2510). The two decide on the device which of them runs: lengths are known there alone.
 #include "paged_prefill.cuh"
